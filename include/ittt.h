@@ -396,6 +396,117 @@ ittt_status ittt_selftest_device_check(const ittt_problem* p, const void* Z, con
 ittt_status ittt_lm_target_noalloc(const ittt_problem* p, const void* X0, const void* conv_kernel,
                                    const void* W_target, void* Vhat, void* stream);
 
+/* ------------------------------------------------- around the layer
+ * The operators a model needs next to the fast-weight MLP: the plain products
+ * of its other layers and projections, and a token mixer that, like the layer,
+ * is linear in the sequence length and carries a state from segment to segment
+ * and into decoding.  Inference only, as everything here.  The conventions
+ * above hold, with these differences: matrices whose rows are tokens may be
+ * column slices of wider ones (a row stride in elements; 0 = dense rows), and
+ * optional tensors are passed as NULL. */
+
+typedef enum {
+  ITTT_ACT_NONE = 0,
+  ITTT_ACT_RELU = 1,
+  ITTT_ACT_SILU = 2,      /* x / (1 + e^-x)                                        */
+  ITTT_ACT_GELU = 3,      /* x (1 + erf(x / sqrt 2)) / 2                           */
+  ITTT_ACT_GELU_TANH = 4  /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2       */
+} ittt_act;
+
+typedef struct {
+  int64_t M;       /* rows (tokens)                                               */
+  int64_t N;       /* output columns                                              */
+  int64_t K;       /* contracted columns                                          */
+  int64_t ldx;     /* elements between rows of X, >= K; 0 = K                      */
+  int64_t ldr;     /* elements between rows of the residual, >= N; 0 = N           */
+  int64_t ldy;     /* elements between rows of Y, >= N; 0 = N                      */
+  int32_t dtype;   /* ittt_dtype of every tensor                                  */
+  int32_t act;     /* ittt_act                                                    */
+} ittt_linear_problem;
+
+/* Bytes of workspace ittt_linear needs for *p on the current device (0 for
+ * most shapes; products with few output tiles split K over CTAs and keep the
+ * partial sums there).  Validates *p like the call. */
+ittt_status ittt_linear_workspace_size(const ittt_linear_problem* p, size_t* bytes);
+
+/* Y = act(X W^T + bias) + residual.
+ * X [M, K]; W [N, K] (nn.Linear layout); bias [N] or NULL; residual [M, N] or
+ * NULL, may be Y itself (with ldr = ldy) and must not overlap Y otherwise;
+ * Y [M, N].  Sums are held in fp32 and the epilogue computes in fp32 with one
+ * rounding on the store.  bf16: K % 8 == 0, ldx % 8 == 0, X and W 16-byte
+ * aligned (else ITTT_ERR_UNSUPPORTED); M, N, ldr and ldy are free.  f32: any
+ * sizes.  The result does not depend on what ran before or beside the call. */
+ittt_status ittt_linear(const ittt_linear_problem* p, const void* X, const void* W,
+                        const void* bias, const void* residual, void* Y, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int64_t B;       /* sequences                                                   */
+  int64_t T;       /* tokens per sequence in this call (1 = a decode step)        */
+  int64_t d;       /* channels                                                    */
+  int64_t ldx;     /* elements between tokens of X, >= d; 0 = d; sequences T ldx apart */
+  int64_t ldy;     /* the same of Y                                               */
+  int32_t k;       /* taps, 1..16                                                 */
+  int32_t dtype;   /* ittt_dtype of every tensor                                  */
+  int32_t act;     /* ittt_act                                                    */
+  int32_t reserved;/* must be 0                                                   */
+} ittt_conv_problem;
+
+/* The short causal convolution of a token mixer, the mirror of
+ * ittt_lookahead_conv (each channel on its own, over the tokens before):
+ *   Y[b, t, c] = act(bias[c] + sum_j conv_kernel[c, j] X[b, t - (k - 1) + j, c])
+ * so tap k - 1 multiplies the token itself.  Tokens before the call's first
+ * come from state_in [B, k - 1, d] (oldest first; NULL: zeros); state_out
+ * [B, k - 1, d] (NULL: not wanted) gets the last k - 1 inputs of each sequence,
+ * the next call's state_in, and may be state_in itself.
+ * conv_kernel [d, k]; bias [d] or NULL; lengths: int32 [B] on the device or
+ * NULL: sequence b has lengths[b] tokens in this call (clamped to 0..T); the
+ * rows behind them are not read, and their rows of Y are left as they were.
+ * Y must not overlap X or the states.  One rounding, on the store. */
+ittt_status ittt_causal_conv(const ittt_conv_problem* p, const void* X, const void* conv_kernel,
+                             const void* bias, const void* state_in, const int32_t* lengths,
+                             void* Y, void* state_out, void* stream);
+
+/* Bits of ittt_scan_problem.flags: the step size is softplus(delta + dt_bias). */
+#define ITTT_SCAN_SOFTPLUS 1
+
+typedef struct {
+  int64_t B;       /* sequences                                                   */
+  int64_t T;       /* tokens per sequence in this call (1 = a decode step)        */
+  int64_t d;       /* channels                                                    */
+  int64_t ldu, ldt, ldb, ldc, ldz, ldy; /* elements between tokens of U, delta, Bm,
+                      Cm, Z and Y (>= d; Bm and Cm >= G N); 0 = dense; sequences are
+                      T times as far apart                                         */
+  int32_t N;       /* state elements per channel, 1..256                          */
+  int32_t G;       /* groups of d / G channels that share Bm and Cm; d % G == 0    */
+  int32_t dtype;   /* ittt_dtype of U, delta, Bm, Cm, Z, Y                         */
+  int32_t flags;   /* ITTT_SCAN_* bits, others must be 0                          */
+} ittt_scan_problem;
+
+/* Bytes of workspace ittt_selective_scan needs for *p on the current device (0
+ * unless the call is split over time: few channels and many tokens).
+ * Validates *p like the call. */
+ittt_status ittt_selective_scan_workspace_size(const ittt_scan_problem* p, size_t* bytes);
+
+/* The selective state space scan.  Per sequence, channel c (of group g) and
+ * state element n, with s_t = delta_t + dt_bias, or softplus of that:
+ *   h_t[c, n] = exp(s_t[c] A[c, n]) h_(t-1)[c, n] + s_t[c] U_t[c] Bm_t[g, n]
+ *   y_t[c]    = sum_n h_t[c, n] Cm_t[g, n] + D[c] U_t[c]
+ *   Y_t[c]    = y_t[c] silu(Z_t[c])
+ * U, delta, Z (or NULL: no gate), Y [B, T, d] and Bm, Cm [B, T, G, N] of dtype;
+ * A [d, N], D [d] or NULL, dt_bias [d] or NULL float32; state_in [B, d, N]
+ * float32 (NULL: zeros) is h before the call's first token, state_out [B, d, N]
+ * float32 (NULL: not wanted) h after each sequence's last one, and may be
+ * state_in itself.  lengths as for ittt_causal_conv (a sequence of length 0
+ * passes its state through).  Y must not overlap an input.  Everything is
+ * computed and held in fp32; Y is rounded once.  Values that the formulas take
+ * out of range come out inf or NaN as they would there. */
+ittt_status ittt_selective_scan(const ittt_scan_problem* p, const void* U, const void* delta,
+                                const float* A, const void* Bm, const void* Cm, const float* D,
+                                const float* dt_bias, const void* Z, const float* state_in,
+                                const int32_t* lengths, void* Y, float* state_out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

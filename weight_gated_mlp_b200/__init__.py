@@ -19,6 +19,10 @@ LIB_PATH = os.path.join(PKG, "libittt.so")
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_DEVICE_FAULT = range(7)
 FLAG_PAD_CHUNK_END, FLAG_X0_LOOKAHEAD = 1, 2
 F32, BF16 = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
+_ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU,
+         "gelu_tanh": ACT_GELU_TANH}
+SCAN_SOFTPLUS = 1
 FORM_AUTO, FORM_PREFIX, FORM_DUAL, FORM_HYBRID = 0, 1, 2, 3
 _FORMS = {"auto": FORM_AUTO, "prefix": FORM_PREFIX, "dual": FORM_DUAL, "hybrid": FORM_HYBRID}
 
@@ -31,7 +35,8 @@ EXPORTED = (
     "ittt_decode_step", "ittt_cp_workspace_size", "ittt_cp_delta", "ittt_cp_apply",
     "ittt_cp_prefix", "ittt_probe_start", "ittt_probe_read", "ittt_set_checks",
     "ittt_check_buffer", "ittt_resolve_form", "ittt_selftest_device_check",
-    "ittt_chunk_recurrence", "ittt_probe_read2",
+    "ittt_chunk_recurrence", "ittt_probe_read2", "ittt_linear_workspace_size", "ittt_linear",
+    "ittt_causal_conv", "ittt_selective_scan_workspace_size", "ittt_selective_scan",
 )
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
@@ -47,6 +52,26 @@ class Problem(ctypes.Structure):
                 ("f", ctypes.c_int64), ("C", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("eta", ctypes.c_float), ("dtype", ctypes.c_int32), ("form", ctypes.c_int32),
                 ("flags", ctypes.c_int32), ("clip", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class LinearProblem(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class ConvProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("k", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ScanProblem(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("T", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("ldu", ctypes.c_int64), ("ldt", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldc", ctypes.c_int64), ("ldz", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("N", ctypes.c_int32), ("G", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -91,6 +116,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "ittt_resolve_form": ([P, ctypes.POINTER(ctypes.c_int32)], i32),
         "ittt_probe_read": ([vp, i32, ctypes.POINTER(ctypes.c_int)], i32),
         "ittt_probe_read2": ([vp, vp, i32, ctypes.POINTER(ctypes.c_int)], i32),
+        "ittt_linear_workspace_size": ([ctypes.POINTER(LinearProblem),
+                                        ctypes.POINTER(ctypes.c_size_t)], i32),
+        "ittt_linear": ([ctypes.POINTER(LinearProblem)] + [vp] * 6 + [ctypes.c_size_t, vp], i32),
+        "ittt_causal_conv": ([ctypes.POINTER(ConvProblem)] + [vp] * 8, i32),
+        "ittt_selective_scan_workspace_size": ([ctypes.POINTER(ScanProblem),
+                                                ctypes.POINTER(ctypes.c_size_t)], i32),
+        "ittt_selective_scan": ([ctypes.POINTER(ScanProblem)] + [vp] * 13 + [ctypes.c_size_t, vp],
+                                i32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -407,6 +440,244 @@ class Decoder:
         self.graphs[self.pos % self.p.C].replay()
         self.pos += 1
         return self.O_out
+
+
+# ------------------------------------------------------------ around the layer
+
+class _OnDevice:
+    """The device of a call's tensors made current while the call runs (nothing
+    where it is already), and the raw handle of its stream."""
+
+    __slots__ = ("dev", "before", "stream")
+
+    def __init__(self, t, stream):
+        torch = _torch()
+        if not t.is_cuda:
+            raise ValueError("the operands must be CUDA tensors")
+        self.dev = t.device.index
+        self.before = torch._C._cuda_getDevice()
+        self.stream = stream
+
+    def __enter__(self):
+        torch = _torch()
+        if self.before != self.dev:
+            torch.cuda.set_device(self.dev)
+        if self.stream is not None:
+            return int(self.stream.cuda_stream) or None
+        return torch._C._cuda_getCurrentRawStream(self.dev) or None
+
+    def __exit__(self, *exc):
+        if self.before != self.dev:
+            _torch().cuda.set_device(self.before)
+
+
+def _same(t, name: str, shape, dtype, device) -> int:
+    """The address of a dense tensor of this shape, type and device."""
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        _check_tensor(t, name, shape, dtype)
+    return t.data_ptr()
+
+
+def _rows(t, name: str, shape, dtype, device) -> Tuple[int, int]:
+    """(address, elements between rows) of a [..., width] tensor whose rows are a
+    fixed distance apart (dense, or a column slice of a dense tensor)."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    width = shape[-1]
+    ld, step, ok = None, 0, t.stride(-1) == 1 or width == 1
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = step = stride
+        ok = ok and stride == step
+        step *= size
+    ld = width if ld is None else ld
+    if not ok or ld < width:
+        raise ValueError(f"{name} must be dense, or a column slice of a dense tensor "
+                         f"(shape {tuple(t.shape)}, strides {t.stride()})")
+    return t.data_ptr(), ld
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tensors made here for work on another stream than the current one: their
+    memory is not given out again before that work is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _act_of(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"unknown activation {act!r}, expected one of {sorted(_ACTS)}")
+    return _ACTS[act]
+
+
+def linear(X, W, bias=None, residual=None, act: str = "none", out=None, workspace=None, stream=None):
+    """act(X W^T + bias) + residual, computed in fp32 and rounded once.
+
+    X: [..., K] (dense, or a column slice of a dense tensor); W: [N, K]; bias:
+    [N]; residual and out: [..., N], rows a fixed distance apart, may be the
+    same tensor; all of one dtype (bf16 with K % 8 == 0, or fp32).  act: "none",
+    "relu", "silu", "gelu" or "gelu_tanh".  workspace: uint8 tensor of at least
+    ittt_linear_workspace_size bytes (allocated where missing).
+    """
+    torch = _torch()
+    lib = load_library()
+    dt, dev = X.dtype, X.device
+    code = _dtype_name(X)
+    if X.dim() < 1 or W.dim() != 2:
+        raise ValueError("X must have shape [..., K] and W [N, K]")
+    N, K = W.shape
+    if X.shape[-1] != K:
+        raise ValueError(f"X has {X.shape[-1]} columns, W {K}")
+    shape = X.shape[:-1] + (N,)
+    M = 1
+    for n in X.shape[:-1]:
+        M *= n
+    with _OnDevice(X, stream) as st:
+        made = None
+        if out is None:
+            out = made = torch.empty(shape, dtype=dt, device=dev)
+            y, ldy = out.data_ptr(), 0
+        else:
+            y, ldy = _rows(out, "out", shape, dt, dev)
+        x, ldx = _rows(X, "X", X.shape, dt, dev)
+        r, ldr = _rows(residual, "residual", shape, dt, dev) if residual is not None else (None, 0)
+        p = LinearProblem(M, N, K, ldx, ldr, ldy, BF16 if code == "bf16" else F32, _act_of(act))
+        ref = ctypes.byref(p)
+        w = _same(W, "W", (N, K), dt, dev)
+        b = _same(bias, "bias", (N,), dt, dev) if bias is not None else None
+        n = ctypes.c_size_t(0)
+        _check(lib.ittt_linear_workspace_size(ref, ctypes.byref(n)), "ittt_linear_workspace_size")
+        need, scratch = n.value, None
+        if need and (workspace is None or workspace.numel() < need):
+            workspace = scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws, size = (workspace.data_ptr(), workspace.numel()) if need else (None, 0)
+        _used_on(stream, made, scratch)
+        _check(lib.ittt_linear(ref, x, w, b, r, y, ws, size, st), "ittt_linear")
+    return out
+
+
+def causal_conv(X, conv_kernel, bias=None, act: str = "none", state=None, lengths=None, out=None,
+                state_out=None, stream=None) -> Tuple["object", "object"]:
+    """(Y [B, T, d], state [B, k - 1, d]) of the depthwise convolution over each
+    token and the k - 1 before it: Y[t, c] = act(bias[c] + sum_j conv_kernel[c, j]
+    X[t - (k - 1) + j, c]).
+
+    X: [B, T, d] (dense, or a column slice of a dense tensor); conv_kernel: [d, k];
+    bias: [d]; state: [B, k - 1, d], the inputs before the first token (None:
+    zeros), the returned state of the segment before; state_out may be the same
+    tensor.  T = 1 is a decode step.  lengths: int32 [B], the tokens of each
+    sequence of a padded batch; rows of Y behind them are left as they were
+    (what ``out`` held).
+    """
+    torch = _torch()
+    lib = load_library()
+    dt, dev = X.dtype, X.device
+    code = _dtype_name(X)
+    if X.dim() != 3 or conv_kernel.dim() != 2:
+        raise ValueError("X must have shape [B, T, d] and conv_kernel [d, k]")
+    B, T, d = X.shape
+    k = conv_kernel.shape[1]
+    with _OnDevice(X, stream) as st:
+        made = made_state = None
+        if out is None:
+            # rows behind a sequence's end are not written: they come out as zeros
+            out = made = (torch.empty if lengths is None else torch.zeros)((B, T, d), dtype=dt, device=dev)
+            y, ldy = out.data_ptr(), 0
+        else:
+            y, ldy = _rows(out, "out", X.shape, dt, dev)
+        if state_out is None:
+            state_out = made_state = torch.empty((B, k - 1, d), dtype=dt, device=dev)
+        x, ldx = _rows(X, "X", X.shape, dt, dev)
+        p = ConvProblem(B, T, d, ldx, ldy, k, BF16 if code == "bf16" else F32, _act_of(act), 0)
+        w = _same(conv_kernel, "conv_kernel", (d, k), dt, dev)
+        b = _same(bias, "bias", (d,), dt, dev) if bias is not None else None
+        s = _same(state, "state", (B, k - 1, d), dt, dev) if state is not None else None
+        so = _same(state_out, "state_out", (B, k - 1, d), dt, dev)
+        n = _same(lengths, "lengths", (B,), torch.int32, dev) if lengths is not None else None
+        _used_on(stream, made, made_state)
+        _check(lib.ittt_causal_conv(ctypes.byref(p), x, w, b, s, n, y, so, st), "ittt_causal_conv")
+    return out, state_out
+
+
+def selective_scan(U, delta, A, Bm, Cm, D=None, Z=None, dt_bias=None, dt_softplus: bool = False,
+                   state=None, lengths=None, out=None, state_out=None, workspace=None, stream=None
+                   ) -> Tuple["object", "object"]:
+    """(Y [B, T, d], state [B, d, N] fp32) of the selective state space scan:
+    h_t = exp(s_t A) h_(t-1) + s_t U_t Bm_t, Y_t = (h_t . Cm_t + D U_t) silu(Z_t),
+    with the step size s = delta + dt_bias, or its softplus.
+
+    U, delta, Z: [B, T, d]; Bm, Cm: [B, T, N], or [B, T, G, N] for G groups of
+    d / G channels; all of one dtype (bf16 or fp32), dense or column slices of
+    dense tensors.  A: [d, N], D, dt_bias: [d], fp32.  state: [B, d, N] fp32, h
+    before the first token (None: zeros); state_out may be the same tensor.  T =
+    1 is a decode step.  lengths: int32 [B], as for ``causal_conv``.
+    """
+    torch = _torch()
+    lib = load_library()
+    dt, dev = U.dtype, U.device
+    code = _dtype_name(U)
+    if U.dim() != 3 or A.dim() != 2 or Bm.dim() not in (3, 4):
+        raise ValueError("U must have shape [B, T, d], A [d, N], Bm and Cm [B, T, N] or [B, T, G, N]")
+    B, T, d = U.shape
+    N = A.shape[1]
+    G = Bm.shape[2] if Bm.dim() == 4 else 1
+    f32 = torch.float32
+    if Bm.dim() == 4:
+        for t, name in ((Bm, "Bm"), (Cm, "Cm")):
+            if t.dim() == 4 and G > 1 and (t.stride(3) != 1 and N > 1 or t.stride(2) != N):
+                raise ValueError(f"the groups of {name} must stand side by side (strides {t.stride()})")
+    with _OnDevice(U, stream) as st:
+        made = made_state = scratch = None
+        if out is None:
+            out = made = (torch.empty if lengths is None else torch.zeros)((B, T, d), dtype=dt, device=dev)
+            y, ldy = out.data_ptr(), 0
+        else:
+            y, ldy = _rows(out, "out", U.shape, dt, dev)
+        if state_out is None:
+            state_out = made_state = torch.empty((B, d, N), dtype=f32, device=dev)
+        u, ldu = _rows(U, "U", U.shape, dt, dev)
+        dl, ldt = _rows(delta, "delta", U.shape, dt, dev)
+        z, ldz = _rows(Z, "Z", U.shape, dt, dev) if Z is not None else (None, 0)
+        bc = []
+        for t, name in ((Bm, "Bm"), (Cm, "Cm")):
+            want = (B, T, G, N) if Bm.dim() == 4 else (B, T, N)
+            if t.shape != want:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {want}")
+            if len(want) == 4:
+                t = t.squeeze(2) if G == 1 else t.as_strided((B, T, G * N), t.stride()[:2] + (1,))
+            bc += _rows(t, name, (B, T, G * N), dt, dev)
+        p = ScanProblem(B, T, d, ldu, ldt, bc[1], bc[3], ldz, ldy, N, G,
+                        BF16 if code == "bf16" else F32, SCAN_SOFTPLUS if dt_softplus else 0)
+        ref = ctypes.byref(p)
+        a = _same(A, "A", (d, N), f32, dev)
+        sk = _same(D, "D", (d,), f32, dev) if D is not None else None
+        db = _same(dt_bias, "dt_bias", (d,), f32, dev) if dt_bias is not None else None
+        s = _same(state, "state", (B, d, N), f32, dev) if state is not None else None
+        so = _same(state_out, "state_out", (B, d, N), f32, dev)
+        n = _same(lengths, "lengths", (B,), torch.int32, dev) if lengths is not None else None
+        need = ctypes.c_size_t(0)
+        _check(lib.ittt_selective_scan_workspace_size(ref, ctypes.byref(need)),
+               "ittt_selective_scan_workspace_size")
+        need = need.value
+        if need and (workspace is None or workspace.numel() < need):
+            workspace = scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws, size = (workspace.data_ptr(), workspace.numel()) if need else (None, 0)
+        _used_on(stream, made, made_state, scratch)
+        _check(lib.ittt_selective_scan(ref, u, dl, a, bc[0], bc[2], sk, db, z, s, n, y, so, ws, size,
+                                       st), "ittt_selective_scan")
+    return out, state_out
 
 
 # ------------------------------------------------------------ context parallel

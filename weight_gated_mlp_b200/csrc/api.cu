@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "mixer.cuh"
 #include "simt.cuh"
 #include "tc_gemm.cuh"
 #include "tc_recur.cuh"
@@ -2342,3 +2343,5 @@ ittt_status ittt_selftest_wait_timeout(uint64_t ns, void* stream) {
 }
 
 }  // extern "C"
+
+#include "mixer_api.cuh"

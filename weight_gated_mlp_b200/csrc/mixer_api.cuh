@@ -1,0 +1,263 @@
+// C ABI of the operators around the layer (validation and dispatch of the
+// kernels of mixer.cuh).  Included at the end of api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+bool valid_dtype_act(int32_t dtype, int32_t act) {
+  return (dtype == ITTT_F32 || dtype == ITTT_BF16) && act >= ITTT_ACT_NONE &&
+         act <= ITTT_ACT_GELU_TANH;
+}
+
+// The row stride that 0 stands for.
+long long stride_or(int64_t ld, int64_t dense) { return ld == 0 ? dense : ld; }
+
+// Bytes from the first to the last element of `rows` rows of `width` elements,
+// `ld` apart.
+size_t span_bytes(long long rows, long long ld, long long width, size_t es) {
+  return (size_t(rows - 1) * size_t(ld) + size_t(width)) * es;
+}
+
+// Row counts and widths fit 32 bits, a whole matrix fits 2^62 bytes.
+bool fits(int64_t rows, int64_t width, int64_t ld) {
+  constexpr int64_t k31 = 1ll << 31;
+  return rows > 0 && width > 0 && rows < k31 && width < k31 && (ld == 0 || (ld >= width && ld < k31));
+}
+
+// ------------------------------------------------------------------ linear
+
+ittt_status validate_linear(const ittt_linear_problem* p) {
+  if (!p || p->M <= 0 || p->N <= 0 || p->K <= 0 || p->ldx < 0 || p->ldr < 0 || p->ldy < 0 ||
+      !valid_dtype_act(p->dtype, p->act))
+    return ITTT_ERR_INVALID_ARG;
+  if ((p->ldx && p->ldx < p->K) || (p->ldr && p->ldr < p->N) || (p->ldy && p->ldy < p->N))
+    return ITTT_ERR_INVALID_ARG;
+  if (!fits(p->M, p->K, p->ldx) || !fits(p->M, p->N, p->ldr) || !fits(p->M, p->N, p->ldy))
+    return ITTT_ERR_UNSUPPORTED;
+  if (p->dtype == ITTT_BF16 && (p->K % 8 || p->ldx % 8)) return ITTT_ERR_UNSUPPORTED;
+  return ITTT_OK;
+}
+
+template <typename T_>
+ittt_status linear_launch(const ittt_linear_problem* p, const void* X, const void* W,
+                          const void* bias, const void* residual, void* Y, cudaStream_t st) {
+  LinearArgs<T_> a{};
+  a.X = static_cast<const T_*>(X);
+  a.W = static_cast<const T_*>(W);
+  a.bias = static_cast<const T_*>(bias);
+  a.residual = static_cast<const T_*>(residual);
+  a.Y = static_cast<T_*>(Y);
+  a.ldx = stride_or(p->ldx, p->K);
+  a.ldr = stride_or(p->ldr, p->N);
+  a.ldy = stride_or(p->ldy, p->N);
+  a.M = int(p->M);
+  a.N = int(p->N);
+  a.K = int(p->K);
+  a.act = p->act;
+  const long long gy = cdiv(p->M, 64);
+  if (gy > 65535) return ITTT_ERR_UNSUPPORTED;
+  return launch_pdl(linear_simt_kernel<T_>, dim3(unsigned(cdiv(p->N, 64)), unsigned(gy)), dim3(256),
+                    st, a);
+}
+
+// ------------------------------------------------------------- causal conv
+
+ittt_status validate_conv(const ittt_conv_problem* p) {
+  if (!p || p->B <= 0 || p->T <= 0 || p->d <= 0 || p->k <= 0 || p->ldx < 0 || p->ldy < 0 ||
+      p->reserved != 0 || !valid_dtype_act(p->dtype, p->act))
+    return ITTT_ERR_INVALID_ARG;
+  if ((p->ldx && p->ldx < p->d) || (p->ldy && p->ldy < p->d)) return ITTT_ERR_INVALID_ARG;
+  if (p->k > 16 || p->B > 65535 || p->T >= (1ll << 31) || p->B * p->T >= (1ll << 31) ||
+      !fits(p->B * p->T, p->d, p->ldx) || !fits(p->B * p->T, p->d, p->ldy))
+    return ITTT_ERR_UNSUPPORTED;
+  return ITTT_OK;
+}
+
+template <typename T_>
+ittt_status causal_conv_launch(const ittt_conv_problem* p, const void* X, const void* w,
+                               const void* bias, const void* state_in, const int32_t* lengths,
+                               void* Y, void* state_out, cudaStream_t st) {
+  CausalConvArgs<T_> a{};
+  a.X = static_cast<const T_*>(X);
+  a.w = static_cast<const T_*>(w);
+  a.bias = static_cast<const T_*>(bias);
+  a.state_in = p->k > 1 ? static_cast<const T_*>(state_in) : nullptr;
+  a.lengths = lengths;
+  a.Y = static_cast<T_*>(Y);
+  a.state_out = p->k > 1 ? static_cast<T_*>(state_out) : nullptr;
+  a.ldx = stride_or(p->ldx, p->d);
+  a.ldy = stride_or(p->ldy, p->d);
+  a.B = int(p->B);
+  a.T = int(p->T);
+  a.d = int(p->d);
+  a.k = p->k;
+  a.act = p->act;
+  const long long rest = p->T - (p->k - 1);
+  const long long gy = 1 + (rest > 0 ? cdiv(rest, 16) : 0);
+  if (gy > 65535) return ITTT_ERR_UNSUPPORTED;
+  return launch_pdl(causal_conv_kernel<T_>,
+                    dim3(unsigned(cdiv(p->d, 256)), unsigned(gy), unsigned(p->B)), dim3(256), st, a);
+}
+
+// ---------------------------------------------------------- selective scan
+
+ittt_status validate_scan(const ittt_scan_problem* p) {
+  if (!p || p->B <= 0 || p->T <= 0 || p->d <= 0 || p->N <= 0 || p->G <= 0 ||
+      (p->dtype != ITTT_F32 && p->dtype != ITTT_BF16) || (p->flags & ~ITTT_SCAN_SOFTPLUS) != 0)
+    return ITTT_ERR_INVALID_ARG;
+  const int64_t gn = int64_t(p->G) * p->N;
+  const int64_t ld[] = {p->ldu, p->ldt, p->ldz, p->ldy, p->ldb, p->ldc};
+  for (int i = 0; i < 6; ++i)
+    if (ld[i] < 0 || (ld[i] && ld[i] < (i < 4 ? p->d : gn))) return ITTT_ERR_INVALID_ARG;
+  if (p->d % p->G != 0) return ITTT_ERR_INVALID_ARG;
+  if (p->N > 256 || p->B >= (1ll << 31) || p->T >= (1ll << 31) || p->B * p->T >= (1ll << 31))
+    return ITTT_ERR_UNSUPPORTED;
+  for (int i = 0; i < 6; ++i)
+    if (!fits(p->B * p->T, i < 4 ? p->d : gn, ld[i])) return ITTT_ERR_UNSUPPORTED;
+  if (p->B * p->d >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
+  return ITTT_OK;
+}
+
+template <typename T_>
+ScanArgs<T_> scan_args(const ittt_scan_problem* p, const void* U, const void* delta, const float* A,
+                       const void* Bm, const void* Cm, const float* D, const float* dt_bias,
+                       const void* Z, const float* state_in, const int32_t* lengths, void* Y,
+                       float* state_out) {
+  ScanArgs<T_> a{};
+  a.U = static_cast<const T_*>(U);
+  a.delta = static_cast<const T_*>(delta);
+  a.Bm = static_cast<const T_*>(Bm);
+  a.Cm = static_cast<const T_*>(Cm);
+  a.Z = static_cast<const T_*>(Z);
+  a.A = A;
+  a.D = D;
+  a.dt_bias = dt_bias;
+  a.state_in = state_in;
+  a.lengths = lengths;
+  a.Y = static_cast<T_*>(Y);
+  a.state_out = state_out;
+  const long long gn = (long long)p->G * p->N;
+  a.ldu = stride_or(p->ldu, p->d);
+  a.ldt = stride_or(p->ldt, p->d);
+  a.ldb = stride_or(p->ldb, gn);
+  a.ldc = stride_or(p->ldc, gn);
+  a.ldz = stride_or(p->ldz, p->d);
+  a.ldy = stride_or(p->ldy, p->d);
+  a.B = int(p->B);
+  a.T = int(p->T);
+  a.d = int(p->d);
+  a.N = p->N;
+  a.G = p->G;
+  a.softplus = p->flags & ITTT_SCAN_SOFTPLUS;
+  return a;
+}
+
+template <typename T_>
+ittt_status scan_launch(const ScanArgs<T_>& a, cudaStream_t st) {
+  return launch_pdl(selective_scan_kernel<T_>, dim3(unsigned(cdiv((long long)a.B * a.d, 4))),
+                    dim3(128), st, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+ittt_status ittt_linear_workspace_size(const ittt_linear_problem* p, size_t* bytes) {
+  if (!bytes) return ITTT_ERR_INVALID_ARG;
+  const ittt_status s = validate_linear(p);
+  if (s != ITTT_OK) return s;
+  *bytes = 0;
+  return ITTT_OK;
+}
+
+ittt_status ittt_linear(const ittt_linear_problem* p, const void* X, const void* W,
+                        const void* bias, const void* residual, void* Y, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const NvtxRange nvtx_range("ittt_linear");
+  ittt_status s = validate_linear(p);
+  if (s != ITTT_OK) return s;
+  if (!X || !W || !Y) return ITTT_ERR_INVALID_ARG;
+  if (residual == Y && stride_or(p->ldr, p->N) != stride_or(p->ldy, p->N)) return ITTT_ERR_INVALID_ARG;
+  const size_t es = p->dtype == ITTT_BF16 ? 2 : 4;
+  if ((s = check_buffers({{X, span_bytes(p->M, stride_or(p->ldx, p->K), p->K, es)},
+                          {W, size_t(p->N) * p->K * es},
+                          {bias, size_t(p->N) * es},
+                          {residual, span_bytes(p->M, stride_or(p->ldr, p->N), p->N, es)},
+                          {Y, span_bytes(p->M, stride_or(p->ldy, p->N), p->N, es)},
+                          {workspace, workspace_bytes}})) != ITTT_OK)
+    return s;
+  if (p->dtype == ITTT_BF16) {
+    if (!aligned16(X) || !aligned16(W)) return ITTT_ERR_UNSUPPORTED;
+    return linear_launch<__nv_bfloat16>(p, X, W, bias, residual, Y, as_stream(stream));
+  }
+  return linear_launch<float>(p, X, W, bias, residual, Y, as_stream(stream));
+}
+
+ittt_status ittt_causal_conv(const ittt_conv_problem* p, const void* X, const void* conv_kernel,
+                             const void* bias, const void* state_in, const int32_t* lengths,
+                             void* Y, void* state_out, void* stream) {
+  const NvtxRange nvtx_range("ittt_causal_conv");
+  ittt_status s = validate_conv(p);
+  if (s != ITTT_OK) return s;
+  if (!X || !conv_kernel || !Y || X == Y) return ITTT_ERR_INVALID_ARG;
+  const size_t es = p->dtype == ITTT_BF16 ? 2 : 4;
+  const long long rows = p->B * p->T;
+  const size_t state = size_t(p->B) * size_t(p->k - 1) * p->d * es;
+  if ((s = check_buffers({{X, span_bytes(rows, stride_or(p->ldx, p->d), p->d, es)},
+                          {conv_kernel, size_t(p->d) * p->k * es},
+                          {bias, size_t(p->d) * es},
+                          {state_in, state},
+                          {lengths, size_t(p->B) * 4},
+                          {Y, span_bytes(rows, stride_or(p->ldy, p->d), p->d, es)},
+                          {state_out, state}})) != ITTT_OK)
+    return s;
+  if (p->dtype == ITTT_BF16)
+    return causal_conv_launch<__nv_bfloat16>(p, X, conv_kernel, bias, state_in, lengths, Y,
+                                             state_out, as_stream(stream));
+  return causal_conv_launch<float>(p, X, conv_kernel, bias, state_in, lengths, Y, state_out,
+                                   as_stream(stream));
+}
+
+ittt_status ittt_selective_scan_workspace_size(const ittt_scan_problem* p, size_t* bytes) {
+  if (!bytes) return ITTT_ERR_INVALID_ARG;
+  const ittt_status s = validate_scan(p);
+  if (s != ITTT_OK) return s;
+  *bytes = 0;
+  return ITTT_OK;
+}
+
+ittt_status ittt_selective_scan(const ittt_scan_problem* p, const void* U, const void* delta,
+                                const float* A, const void* Bm, const void* Cm, const float* D,
+                                const float* dt_bias, const void* Z, const float* state_in,
+                                const int32_t* lengths, void* Y, float* state_out, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  const NvtxRange nvtx_range("ittt_selective_scan");
+  ittt_status s = validate_scan(p);
+  if (s != ITTT_OK) return s;
+  if (!U || !delta || !A || !Bm || !Cm || !Y) return ITTT_ERR_INVALID_ARG;
+  if (Y == U || Y == delta || Y == Z || Y == Bm || Y == Cm) return ITTT_ERR_INVALID_ARG;
+  const size_t es = p->dtype == ITTT_BF16 ? 2 : 4;
+  const long long rows = p->B * p->T, gn = (long long)p->G * p->N;
+  const size_t state = size_t(p->B) * p->d * p->N * 4;
+  if ((s = check_buffers({{U, span_bytes(rows, stride_or(p->ldu, p->d), p->d, es)},
+                          {delta, span_bytes(rows, stride_or(p->ldt, p->d), p->d, es)},
+                          {A, size_t(p->d) * p->N * 4},
+                          {Bm, span_bytes(rows, stride_or(p->ldb, gn), gn, es)},
+                          {Cm, span_bytes(rows, stride_or(p->ldc, gn), gn, es)},
+                          {D, size_t(p->d) * 4},
+                          {dt_bias, size_t(p->d) * 4},
+                          {Z, span_bytes(rows, stride_or(p->ldz, p->d), p->d, es)},
+                          {state_in, state},
+                          {lengths, size_t(p->B) * 4},
+                          {Y, span_bytes(rows, stride_or(p->ldy, p->d), p->d, es)},
+                          {state_out, state},
+                          {workspace, workspace_bytes}})) != ITTT_OK)
+    return s;
+  if (p->dtype == ITTT_BF16)
+    return scan_launch(scan_args<__nv_bfloat16>(p, U, delta, A, Bm, Cm, D, dt_bias, Z, state_in,
+                                                lengths, Y, state_out), as_stream(stream));
+  return scan_launch(scan_args<float>(p, U, delta, A, Bm, Cm, D, dt_bias, Z, state_in, lengths, Y,
+                                      state_out), as_stream(stream));
+}
+
+}  // extern "C"
