@@ -424,11 +424,6 @@ typedef struct {
   int32_t act;     /* ittt_act                                                    */
 } ittt_linear_problem;
 
-/* Bytes of workspace ittt_linear needs for *p on the current device (0 for
- * most shapes; products with few output tiles split K over CTAs and keep the
- * partial sums there).  Validates *p like the call. */
-ittt_status ittt_linear_workspace_size(const ittt_linear_problem* p, size_t* bytes);
-
 /* Y = act(X W^T + bias) + residual.
  * X [M, K]; W [N, K] (nn.Linear layout); bias [N] or NULL; residual [M, N] or
  * NULL, may be Y itself (with ldr = ldy) and must not overlap Y otherwise;
@@ -437,8 +432,7 @@ ittt_status ittt_linear_workspace_size(const ittt_linear_problem* p, size_t* byt
  * aligned (else ITTT_ERR_UNSUPPORTED); M, N, ldr and ldy are free.  f32: any
  * sizes.  The result does not depend on what ran before or beside the call. */
 ittt_status ittt_linear(const ittt_linear_problem* p, const void* X, const void* W,
-                        const void* bias, const void* residual, void* Y, void* workspace,
-                        size_t workspace_bytes, void* stream);
+                        const void* bias, const void* residual, void* Y, void* stream);
 
 typedef struct {
   int64_t B;       /* sequences                                                   */

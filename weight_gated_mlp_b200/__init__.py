@@ -35,7 +35,7 @@ EXPORTED = (
     "ittt_decode_step", "ittt_cp_workspace_size", "ittt_cp_delta", "ittt_cp_apply",
     "ittt_cp_prefix", "ittt_probe_start", "ittt_probe_read", "ittt_set_checks",
     "ittt_check_buffer", "ittt_resolve_form", "ittt_selftest_device_check",
-    "ittt_chunk_recurrence", "ittt_probe_read2", "ittt_linear_workspace_size", "ittt_linear",
+    "ittt_chunk_recurrence", "ittt_probe_read2", "ittt_linear",
     "ittt_causal_conv", "ittt_selective_scan_workspace_size", "ittt_selective_scan",
 )
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -116,9 +116,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "ittt_resolve_form": ([P, ctypes.POINTER(ctypes.c_int32)], i32),
         "ittt_probe_read": ([vp, i32, ctypes.POINTER(ctypes.c_int)], i32),
         "ittt_probe_read2": ([vp, vp, i32, ctypes.POINTER(ctypes.c_int)], i32),
-        "ittt_linear_workspace_size": ([ctypes.POINTER(LinearProblem),
-                                        ctypes.POINTER(ctypes.c_size_t)], i32),
-        "ittt_linear": ([ctypes.POINTER(LinearProblem)] + [vp] * 6 + [ctypes.c_size_t, vp], i32),
+        "ittt_linear": ([ctypes.POINTER(LinearProblem)] + [vp] * 6, i32),
         "ittt_causal_conv": ([ctypes.POINTER(ConvProblem)] + [vp] * 8, i32),
         "ittt_selective_scan_workspace_size": ([ctypes.POINTER(ScanProblem),
                                                 ctypes.POINTER(ctypes.c_size_t)], i32),
@@ -522,14 +520,13 @@ def _act_of(act: str) -> int:
     return _ACTS[act]
 
 
-def linear(X, W, bias=None, residual=None, act: str = "none", out=None, workspace=None, stream=None):
+def linear(X, W, bias=None, residual=None, act: str = "none", out=None, stream=None):
     """act(X W^T + bias) + residual, computed in fp32 and rounded once.
 
     X: [..., K] (dense, or a column slice of a dense tensor); W: [N, K]; bias:
     [N]; residual and out: [..., N], rows a fixed distance apart, may be the
     same tensor; all of one dtype (bf16 with K % 8 == 0, or fp32).  act: "none",
-    "relu", "silu", "gelu" or "gelu_tanh".  workspace: uint8 tensor of at least
-    ittt_linear_workspace_size bytes (allocated where missing).
+    "relu", "silu", "gelu" or "gelu_tanh".
     """
     torch = _torch()
     lib = load_library()
@@ -554,17 +551,10 @@ def linear(X, W, bias=None, residual=None, act: str = "none", out=None, workspac
         x, ldx = _rows(X, "X", X.shape, dt, dev)
         r, ldr = _rows(residual, "residual", shape, dt, dev) if residual is not None else (None, 0)
         p = LinearProblem(M, N, K, ldx, ldr, ldy, BF16 if code == "bf16" else F32, _act_of(act))
-        ref = ctypes.byref(p)
         w = _same(W, "W", (N, K), dt, dev)
         b = _same(bias, "bias", (N,), dt, dev) if bias is not None else None
-        n = ctypes.c_size_t(0)
-        _check(lib.ittt_linear_workspace_size(ref, ctypes.byref(n)), "ittt_linear_workspace_size")
-        need, scratch = n.value, None
-        if need and (workspace is None or workspace.numel() < need):
-            workspace = scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws, size = (workspace.data_ptr(), workspace.numel()) if need else (None, 0)
-        _used_on(stream, made, scratch)
-        _check(lib.ittt_linear(ref, x, w, b, r, y, ws, size, st), "ittt_linear")
+        _used_on(stream, made)
+        _check(lib.ittt_linear(ctypes.byref(p), x, w, b, r, y, st), "ittt_linear")
     return out
 
 

@@ -16,6 +16,7 @@
 #include "mixer.cuh"
 #include "simt.cuh"
 #include "tc_gemm.cuh"
+#include "tc_linear.cuh"
 #include "tc_recur.cuh"
 #include "tc_tconv.cuh"
 

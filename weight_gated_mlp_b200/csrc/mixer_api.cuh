@@ -39,8 +39,8 @@ ittt_status validate_linear(const ittt_linear_problem* p) {
 }
 
 template <typename T_>
-ittt_status linear_launch(const ittt_linear_problem* p, const void* X, const void* W,
-                          const void* bias, const void* residual, void* Y, cudaStream_t st) {
+LinearArgs<T_> linear_args(const ittt_linear_problem* p, const void* X, const void* W,
+                           const void* bias, const void* residual, void* Y) {
   LinearArgs<T_> a{};
   a.X = static_cast<const T_*>(X);
   a.W = static_cast<const T_*>(W);
@@ -54,10 +54,145 @@ ittt_status linear_launch(const ittt_linear_problem* p, const void* X, const voi
   a.N = int(p->N);
   a.K = int(p->K);
   a.act = p->act;
-  const long long gy = cdiv(p->M, 64);
+  return a;
+}
+
+ittt_status linear_f32(const LinearArgs<float>& a, cudaStream_t st) {
+  const long long gy = cdiv(a.M, 64);
   if (gy > 65535) return ITTT_ERR_UNSUPPORTED;
-  return launch_pdl(linear_simt_kernel<T_>, dim3(unsigned(cdiv(p->N, 64)), unsigned(gy)), dim3(256),
+  return launch_pdl(linear_simt_kernel<float>, dim3(unsigned(cdiv(a.N, 64)), unsigned(gy)), dim3(256),
                     st, a);
+}
+
+// A launch in clusters of `cluster` CTAs, its prologue overlapping the kernel before.
+template <typename... KArgs, typename... Args>
+ittt_status launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned cluster, unsigned threads,
+                            int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = ITTT_PDL;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) != cudaSuccess)
+    return ITTT_ERR_CUDA;
+  return launch_status();
+}
+
+// Dynamic shared memory above the default, granted once per kernel and device.
+template <typename Kern>
+bool grant_smem(Kern kern, int smem, std::atomic<bool>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if (done[dev].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return false;
+  done[dev].store(true, std::memory_order_relaxed);
+  return true;
+}
+
+// One 128 x MT tile per CTA, K split over clusters.  The split is the widest of
+// 1, 2, 4, 8 CTAs that leaves every CTA of the launch resident (two per SM) and
+// at least four k-blocks to each.
+template <int MT>
+ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream_t st) {
+  using S = SplitShape<MT>;
+  static std::atomic<bool> granted[kMaxDevices] = {};
+  auto kern = linear_split_kernel<MT>;
+  if (!grant_smem(kern, S::SMEM, granted)) return ITTT_ERR_CUDA;
+  const int num_kb = int(cdiv(a.K, 64));
+  const long long m_tiles = cdiv(a.M, MT), tiles = m_tiles * cdiv(a.N, 128);
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= 2ll * sms && num_kb >= 4 * splits * 2) splits *= 2;
+  if (tiles * splits >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
+  CUtensorMap w, x;
+  if (!make_map(&w, a.W, a.K, a.N, a.K, 64, 128) || !make_map(&x, a.X, a.K, a.M, a.ldx, 64, MT))
+    return ITTT_ERR_CUDA;
+  return launch_clusters(kern, unsigned(tiles * splits), unsigned(splits), 192, S::SMEM, st, w, x, a,
+                         int(m_tiles), num_kb, g_wait_ns.load());
+}
+
+// CTA pairs of linear_pair_kernel that the current device holds at once (0: none).
+int resident_pairs(int sms) {
+  static std::atomic<bool> granted[kMaxDevices] = {};
+  static std::atomic<int> pairs[kMaxDevices] = {};
+  if (!grant_smem(linear_pair_kernel, kPairSmem, granted)) return 0;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if ((n = pairs[dev].load(std::memory_order_relaxed)) > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(unsigned(2 * (sms / 2)), 1, 1);
+  cfg.blockDim = dim3(192, 1, 1);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel, &cfg) != cudaSuccess || n <= 0) return 0;
+  pairs[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Persistent CTA pairs.
+ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int mt, int pairs, cudaStream_t st) {
+  PairTile t{};
+  t.mt = mt;
+  t.m_tiles = int(cdiv(a.M, mt));
+  t.n_tiles = int(cdiv(a.N, 256));
+  t.num_kb = int(cdiv(a.K, 64));
+  // a group's rows of W (about 32 MiB) stay in L2 while the rows of X pass once
+  const long long tile_bytes = 256ll * a.K * 2;
+  if (tile_bytes * t.n_tiles > (48ll << 20)) t.group_n = int(std::max(1ll, (32ll << 20) / tile_bytes));
+  if ((long long)t.m_tiles * t.n_tiles >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
+  CUtensorMap w, x;
+  if (!make_map(&w, a.W, a.K, a.N, a.K, 64, 128) || !make_map(&x, a.X, a.K, a.M, a.ldx, 64, mt / 2))
+    return ITTT_ERR_CUDA;
+  const long long units = (long long)t.m_tiles * t.n_tiles;
+  return launch_clusters(linear_pair_kernel, unsigned(2 * std::min<long long>(units, pairs)), 2, 192,
+                         kPairSmem, st, w, x, a, t, g_wait_ns.load());
+}
+
+// Up to 128 rows: one narrow tile of all rows per 128 outputs, so that W is read
+// once.  More: pairs when 256 x 256 tiles fill at least three quarters of the
+// SMs, with the tile height (256, 224, ... 128 rows) whose waves of tiles cost
+// least; else 128 x 128 tiles, or 128 x 64 where even eight-fold splits of those
+// leave SMs empty.
+ittt_status linear_bf16(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
+  const int sms = num_sms();
+  if (sms <= 0) return ITTT_ERR_CUDA;
+  if (a.M <= 16) return linear_split<16>(a, sms, st);
+  if (a.M <= 32) return linear_split<32>(a, sms, st);
+  if (a.M <= 64) return linear_split<64>(a, sms, st);
+  if (a.M <= 128) return linear_split<128>(a, sms, st);
+  const int pairs = resident_pairs(sms);
+  if (pairs <= 0) return ITTT_ERR_CUDA;
+  const long long n_tiles = cdiv(a.N, 256);
+  if (n_tiles * cdiv(a.M, 256) * 4 >= pairs * 3) {
+    int best = 256;
+    long long least = -1;
+    for (int mt = 256; mt >= 128; mt -= 32) {
+      // a wave of tiles costs its height, plus a part that does not shrink with it
+      const long long cost = cdiv(n_tiles * cdiv(a.M, mt), pairs) * (mt + 16);
+      if (least < 0 || cost < least) {
+        least = cost;
+        best = mt;
+      }
+    }
+    return linear_pairs(a, best, pairs, st);
+  }
+  if (cdiv(a.N, 128) * cdiv(a.M, 128) * 8 < sms) return linear_split<64>(a, sms, st);
+  return linear_split<128>(a, sms, st);
 }
 
 // ------------------------------------------------------------- causal conv
@@ -162,17 +297,8 @@ ittt_status scan_launch(const ScanArgs<T_>& a, cudaStream_t st) {
 
 extern "C" {
 
-ittt_status ittt_linear_workspace_size(const ittt_linear_problem* p, size_t* bytes) {
-  if (!bytes) return ITTT_ERR_INVALID_ARG;
-  const ittt_status s = validate_linear(p);
-  if (s != ITTT_OK) return s;
-  *bytes = 0;
-  return ITTT_OK;
-}
-
 ittt_status ittt_linear(const ittt_linear_problem* p, const void* X, const void* W,
-                        const void* bias, const void* residual, void* Y, void* workspace,
-                        size_t workspace_bytes, void* stream) {
+                        const void* bias, const void* residual, void* Y, void* stream) {
   const NvtxRange nvtx_range("ittt_linear");
   ittt_status s = validate_linear(p);
   if (s != ITTT_OK) return s;
@@ -183,14 +309,13 @@ ittt_status ittt_linear(const ittt_linear_problem* p, const void* X, const void*
                           {W, size_t(p->N) * p->K * es},
                           {bias, size_t(p->N) * es},
                           {residual, span_bytes(p->M, stride_or(p->ldr, p->N), p->N, es)},
-                          {Y, span_bytes(p->M, stride_or(p->ldy, p->N), p->N, es)},
-                          {workspace, workspace_bytes}})) != ITTT_OK)
+                          {Y, span_bytes(p->M, stride_or(p->ldy, p->N), p->N, es)}})) != ITTT_OK)
     return s;
   if (p->dtype == ITTT_BF16) {
     if (!aligned16(X) || !aligned16(W)) return ITTT_ERR_UNSUPPORTED;
-    return linear_launch<__nv_bfloat16>(p, X, W, bias, residual, Y, as_stream(stream));
+    return linear_bf16(linear_args<__nv_bfloat16>(p, X, W, bias, residual, Y), as_stream(stream));
   }
-  return linear_launch<float>(p, X, W, bias, residual, Y, as_stream(stream));
+  return linear_f32(linear_args<float>(p, X, W, bias, residual, Y), as_stream(stream));
 }
 
 ittt_status ittt_causal_conv(const ittt_conv_problem* p, const void* X, const void* conv_kernel,
