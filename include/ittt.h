@@ -488,7 +488,7 @@ ittt_status ittt_selective_scan_workspace_size(const ittt_scan_problem* p, size_
  *   y_t[c]    = sum_n h_t[c, n] Cm_t[g, n] + D[c] U_t[c]
  *   Y_t[c]    = y_t[c] silu(Z_t[c])
  * U, delta, Z (or NULL: no gate), Y [B, T, d] and Bm, Cm [B, T, G, N] of dtype;
- * A [d, N], D [d] or NULL, dt_bias [d] or NULL float32; state_in [B, d, N]
+ * A [d, N] (finite), D [d] or NULL, dt_bias [d] or NULL float32; state_in [B, d, N]
  * float32 (NULL: zeros) is h before the call's first token, state_out [B, d, N]
  * float32 (NULL: not wanted) h after each sequence's last one, and may be
  * state_in itself.  lengths as for ittt_causal_conv (a sequence of length 0

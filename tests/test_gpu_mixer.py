@@ -215,6 +215,18 @@ def test_scan_long_and_narrow(B, T, d, N, dtype):
     check_scan(v, dtype, lengths=n, out=torch.zeros_like(v["U"]))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [None, [2100, 1024, 1025, 0]])
+def test_scan_long_and_wide(dtype, lengths):
+    """Channel blocks for every CTA and a long prompt: runs handed from CTA to CTA."""
+    v = scan_inputs(4, 2100, 900, 4, 1, dtype, seed=10)
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out = None if lengths is None else torch.full_like(v["U"], 5.0)
+    Y, s = check_scan(v, dtype, lengths=n, out=out)
+    Y2, s2 = ittt.selective_scan(**v, lengths=n, out=None if out is None else out.clone())
+    assert torch.equal(Y, Y2) and torch.equal(s, s2)
+
+
 @pytest.mark.parametrize("cuts", [[1], [7, 8], [64, 200], [128]])
 def test_segments_match_the_whole(cuts):
     """A prompt in pieces, its states carried in place."""

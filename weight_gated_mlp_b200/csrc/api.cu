@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "mixer.cuh"
+#include "scan.cuh"
 #include "simt.cuh"
 #include "tc_gemm.cuh"
 #include "tc_linear.cuh"

@@ -148,74 +148,4 @@ __global__ void __launch_bounds__(256) causal_conv_kernel(const CausalConvArgs<T
   }
 }
 
-// ---------------------------------------------------------- selective scan
-
-template <typename T_>
-struct ScanArgs {
-  const T_ *U, *delta, *Bm, *Cm, *Z;
-  const float *A, *D, *dt_bias, *state_in;
-  const int32_t* lengths;
-  T_* Y;
-  float* state_out;
-  long long ldu, ldt, ldb, ldc, ldz, ldy;
-  int B, T, d, N, G, softplus;
-};
-
-__device__ __forceinline__ float softplus_f32(float x) {
-  return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
-}
-
-// One warp per sequence and channel, lanes over the state (up to 8 elements a
-// lane), token after token.
-template <typename T_>
-__global__ void __launch_bounds__(128) selective_scan_kernel(const ScanArgs<T_> a) {
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  const long long w = blockIdx.x * 4ll + (threadIdx.x >> 5);
-  if (w >= (long long)a.B * a.d) return;
-  const int b = static_cast<int>(w / a.d), c = static_cast<int>(w % a.d);
-  const int g = c / (a.d / a.G);
-  const int len = sequence_length(a.lengths, b, a.T);
-  float h[8], A[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int n = lane + 32 * i;
-    h[i] = (n < a.N && a.state_in) ? a.state_in[w * a.N + n] : 0.f;
-    A[i] = n < a.N ? a.A[(long long)c * a.N + n] : 0.f;
-  }
-  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
-  const float skip = a.D ? a.D[c] : 0.f;
-  const long long row0 = (long long)b * a.T;
-  for (int t = 0; t < len; ++t) {
-    const long long row = row0 + t;
-    const float u = to_f32(a.U[row * a.ldu + c]);
-    float s = to_f32(a.delta[row * a.ldt + c]) + bias;
-    if (a.softplus) s = softplus_f32(s);
-    float y = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int n = lane + 32 * i;
-      if (n >= a.N) break;
-      const float bn = to_f32(a.Bm[row * a.ldb + g * a.N + n]);
-      const float cn = to_f32(a.Cm[row * a.ldc + g * a.N + n]);
-      h[i] = fmaf(expf(s * A[i]), h[i], s * u * bn);
-      y = fmaf(h[i], cn, y);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (a.D) y = fmaf(skip, u, y);
-    if (lane == 0) {
-      if (a.Z) y *= activate(to_f32(a.Z[row * a.ldz + c]), ITTT_ACT_SILU);
-      a.Y[row * a.ldy + c] = from_f32<T_>(y);
-    }
-  }
-  if (a.state_out) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int n = lane + 32 * i;
-      if (n < a.N) a.state_out[w * a.N + n] = h[i];
-    }
-  }
-}
-
 }  // namespace ittt

@@ -287,10 +287,107 @@ ScanArgs<T_> scan_args(const ittt_scan_problem* p, const void* U, const void* de
   return a;
 }
 
+// How a call is cut (see ScanPlan).  short_call: the serial kernel.
+struct ScanCut {
+  bool short_call, chained;
+  int runs, run_tokens, blocks, per_group;
+  size_t flags, carry, step_sum, total;  // workspace offsets and size
+};
+
+ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
+  ScanCut c{};
+  c.short_call = p->T <= 32;
+  if (c.short_call) return c;
+  c.per_group = int(cdiv(p->d / p->G, kScanCh));
+  c.blocks = c.per_group * p->G;
+  const long long groups = p->B * c.blocks, workers = 2ll * sms;
+  const long long chunks = cdiv(p->T, kScanChunk);
+  long long run_chunks = chunks;
+  if (groups * 4 >= workers * 3) {
+    // enough channel blocks for every CTA: runs of 8 chunks, chained, so that the
+    // work is dealt out evenly however many blocks there are
+    c.chained = true;
+    if (groups < 6 * workers) run_chunks = std::min(chunks, 8ll);
+  } else {
+    // few channels: independent runs, two tasks for every CTA, a run of at least two chunks
+    const long long want = std::max(1ll, 2 * workers / groups);
+    run_chunks = std::min(chunks, std::max(2ll, cdiv(chunks, want)));
+  }
+  c.run_tokens = int(run_chunks * kScanChunk);
+  c.runs = int(cdiv(chunks, run_chunks));
+  if (c.runs == 1) return c;
+  const long long np = scan_np(p->N);
+  size_t off = 0;
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  if (c.chained) {
+    c.flags = take(size_t(1 + groups) * 4);
+    c.carry = take(size_t(groups) * kScanCh * np * 4);
+  } else {
+    c.carry = take(size_t(c.runs - 1) * p->B * p->d * p->N * 4);
+    c.step_sum = take(size_t(c.runs - 1) * p->B * p->d * 4);
+  }
+  c.total = off;
+  return c;
+}
+
 template <typename T_>
-ittt_status scan_launch(const ScanArgs<T_>& a, cudaStream_t st) {
-  return launch_pdl(selective_scan_kernel<T_>, dim3(unsigned(cdiv((long long)a.B * a.d, 4))),
-                    dim3(128), st, a);
+ittt_status scan_short(const ScanArgs<T_>& a, cudaStream_t st) {
+  const int npl = a.N <= 128 ? 4 : 8;
+  int lanes = 1;
+  while (lanes * npl < a.N) lanes *= 2;
+  const int aligned = aligned16(a.A) && aligned16(a.state_in) && aligned16(a.state_out);
+  const dim3 grid(unsigned(cdiv((long long)a.B * a.d * lanes, 128)));
+  if (npl == 4) return launch_pdl(scan_serial_kernel<T_, 4>, grid, dim3(128), st, a, lanes, aligned);
+  return launch_pdl(scan_serial_kernel<T_, 8>, grid, dim3(128), st, a, lanes, aligned);
+}
+
+template <typename T_, bool STATE_ONLY>
+ittt_status scan_chunks(const ScanArgs<T_>& a, const ScanPlan& pl, long long tasks, int sms,
+                        cudaStream_t st) {
+  static std::atomic<bool> granted[kMaxDevices] = {};
+  auto kern = scan_chunk_kernel<T_, STATE_ONLY>;
+  if (!grant_smem(kern, scan_smem_bytes(256), granted)) return ITTT_ERR_CUDA;
+  return launch_clusters(kern, unsigned(std::min<long long>(tasks, 2ll * sms)), 1, kScanThreads,
+                         scan_smem_bytes(a.N), st, a, pl, g_wait_ns.load());
+}
+
+template <typename T_>
+ittt_status scan_launch(const ittt_scan_problem* p, const ScanArgs<T_>& a, void* workspace,
+                        size_t workspace_bytes, cudaStream_t st) {
+  const int sms = num_sms();
+  if (sms <= 0) return ITTT_ERR_CUDA;
+  const ScanCut c = scan_cut(p, sms);
+  if (c.total && (!workspace || workspace_bytes < c.total)) return ITTT_ERR_WORKSPACE;
+  if (c.total && !aligned16(workspace)) return ITTT_ERR_UNSUPPORTED;
+  if (c.short_call) return scan_short(a, st);
+  char* ws = static_cast<char*>(workspace);
+  ScanPlan pl{};
+  pl.blocks = c.blocks;
+  pl.per_group = c.per_group;
+  pl.runs = c.runs;
+  pl.run_tokens = c.run_tokens;
+  pl.chained = c.chained;
+  const long long groups = p->B * c.blocks;
+  if (groups * c.runs >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
+  if (c.runs > 1) {
+    pl.carry = reinterpret_cast<float*>(ws + c.carry);
+    if (c.chained) {
+      pl.flags = reinterpret_cast<unsigned*>(ws + c.flags);
+      if (cudaMemsetAsync(pl.flags, 0, size_t(1 + groups) * 4, st) != cudaSuccess) return ITTT_ERR_CUDA;
+    } else {
+      pl.step_sum = reinterpret_cast<float*>(ws + c.step_sum);
+      ittt_status s = scan_chunks<T_, true>(a, pl, groups * (c.runs - 1), sms, st);
+      if (s != ITTT_OK) return s;
+      s = launch_pdl(scan_join_kernel<T_>, dim3(unsigned(cdiv((long long)a.B * a.d * a.N, 256))),
+                     dim3(256), st, a, pl);
+      if (s != ITTT_OK) return s;
+    }
+  }
+  return scan_chunks<T_, false>(a, pl, groups * c.runs, sms, st);
 }
 
 }  // namespace
@@ -347,7 +444,9 @@ ittt_status ittt_selective_scan_workspace_size(const ittt_scan_problem* p, size_
   if (!bytes) return ITTT_ERR_INVALID_ARG;
   const ittt_status s = validate_scan(p);
   if (s != ITTT_OK) return s;
-  *bytes = 0;
+  const int sms = num_sms();
+  if (sms <= 0) return ITTT_ERR_CUDA;
+  *bytes = scan_cut(p, sms).total;
   return ITTT_OK;
 }
 
@@ -379,10 +478,12 @@ ittt_status ittt_selective_scan(const ittt_scan_problem* p, const void* U, const
                           {workspace, workspace_bytes}})) != ITTT_OK)
     return s;
   if (p->dtype == ITTT_BF16)
-    return scan_launch(scan_args<__nv_bfloat16>(p, U, delta, A, Bm, Cm, D, dt_bias, Z, state_in,
-                                                lengths, Y, state_out), as_stream(stream));
-  return scan_launch(scan_args<float>(p, U, delta, A, Bm, Cm, D, dt_bias, Z, state_in, lengths, Y,
-                                      state_out), as_stream(stream));
+    return scan_launch(p, scan_args<__nv_bfloat16>(p, U, delta, A, Bm, Cm, D, dt_bias, Z, state_in,
+                                                   lengths, Y, state_out),
+                       workspace, workspace_bytes, as_stream(stream));
+  return scan_launch(p, scan_args<float>(p, U, delta, A, Bm, Cm, D, dt_bias, Z, state_in, lengths, Y,
+                                         state_out),
+                     workspace, workspace_bytes, as_stream(stream));
 }
 
 }  // extern "C"
