@@ -350,9 +350,9 @@ ittt_status scan_chunks(const ScanArgs<T_>& a, const ScanPlan& pl, long long tas
                         cudaStream_t st) {
   static std::atomic<bool> granted[kMaxDevices] = {};
   auto kern = scan_chunk_kernel<T_, STATE_ONLY>;
-  if (!grant_smem(kern, scan_smem_bytes(256), granted)) return ITTT_ERR_CUDA;
+  if (!grant_smem(kern, scan_smem_bytes<T_>(256), granted)) return ITTT_ERR_CUDA;
   return launch_clusters(kern, unsigned(std::min<long long>(tasks, 2ll * sms)), 1, kScanThreads,
-                         scan_smem_bytes(a.N), st, a, pl, g_wait_ns.load());
+                         scan_smem_bytes<T_>(a.N), st, a, pl, g_wait_ns.load());
 }
 
 template <typename T_>

@@ -36,15 +36,34 @@ struct ScanArgs {
   int B, T, d, N, G, softplus;
 };
 
-// softplus(x) = max(x, 0) + log(1 + e^-|x|).
-__device__ __forceinline__ float softplus_f32(float x) {
-  return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x)));
-}
-
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// softplus(x) = max(x, 0) + log(1 + e^-|x|).  log(1 + e) = e q(e) on [0, 1], q of
+// degree 9 fitted to least relative error (2^-23 in fp32 Horner steps): small
+// steps keep their relative precision, which a logarithm of 1 + e would lose.
+__device__ __forceinline__ float softplus_f32(float x) {
+  const float e = exp2_approx(-kLog2e * fabsf(x));
+  float q = -0.0032440319f;
+  q = fmaf(q, e, 0.0198514927f);
+  q = fmaf(q, e, -0.0569595918f);
+  q = fmaf(q, e, 0.1060366035f);
+  q = fmaf(q, e, -0.1530559659f);
+  q = fmaf(q, e, 0.1967594028f);
+  q = fmaf(q, e, -0.2495413423f);
+  q = fmaf(q, e, 0.3332996368f);
+  q = fmaf(q, e, -0.4999990165f);
+  q = fmaf(q, e, 1.0f);
+  // NaN stays NaN (fmaxf alone would drop it)
+  return fmaf(q, e, x != x ? x : fmaxf(x, 0.f));
+}
+
+// z / (1 + e^-z) by the hardware's quotient (2 ulp; a denominator past 2^126 gives 0).
+__device__ __forceinline__ float silu_gate(float z) {
+  return __fdividef(z, 1.f + exp2_approx(-kLog2e * z));
 }
 
 // Two fp32 values in one 64-bit register and the paired instructions on them
@@ -139,7 +158,7 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, 
     if (t < len && sub == 0 && real) {
       const long long row = row0 + t;
       if (a.D) y = fmaf(skip, u, y);
-      if (a.Z) y *= activate(to_f32(a.Z[row * a.ldz + c]), ITTT_ACT_SILU);
+      if (a.Z) y *= silu_gate(to_f32(a.Z[row * a.ldz + c]));
       a.Y[row * a.ldy + c] = from_f32<T_>(y);
     }
   }
@@ -163,7 +182,7 @@ constexpr int kScanSegs = 16;                     // spans of a chunk
 constexpr int kScanK = 8;                         // tokens a span
 constexpr int kScanChunk = kScanSegs * kScanK;    // tokens a chunk
 constexpr int kScanThreads = kScanCh * kScanSegs;
-constexpr int kScanSlab = 32;                     // state elements of B and C staged at once
+constexpr int kScanSlab = 16;                     // state elements of B and C staged at once
 
 // How the work of a call is cut.  A task is one channel block of one sequence
 // over one run of tokens; tasks are handed out run by run.
@@ -179,72 +198,141 @@ struct ScanPlan {
   unsigned* flags; // chained: [0] the next task, [1 + B blocks] runs finished
 };
 
-__host__ __device__ constexpr int scan_np(int N) { return (N + 3) & ~3; }
+// Rows of the staged tiles: a span's 8 tokens side by side, the spans 16 (raw
+// rows) or 4 (B and C in fp32) elements further apart than that, so that the two
+// spans of a warp read different banks.
+constexpr int kRawSpan = kScanK * kScanCh + 16;
+constexpr int kRawTile = kScanSegs * kRawSpan;        // elements of one of U, delta, Z
+constexpr int kSlabSpan = kScanK * kScanSlab + 4;
+constexpr int kSlabTile = kScanSegs * kSlabSpan;      // fp32 elements of one of B, C
+constexpr int kSlabRaw = kScanChunk * kScanSlab;      // bf16 elements of one of B, C
 
-// Shared memory: B and C tiles, the spans' end states and decays (two buffers),
-// the state and A log2(e) of the CTA's channels.
-__host__ __device__ constexpr int scan_tile_floats(int N) {
-  // 4 floats more a span: the two spans of a warp read different banks
-  return kScanSegs * (kScanK * (scan_np(N) < kScanSlab ? scan_np(N) : kScanSlab) + 4);
-}
-__host__ __device__ constexpr int scan_smem_bytes(int N) {
-  return 4 * (2 * scan_tile_floats(N) + 2 * 2 * kScanThreads * 4 + 2 * kScanCh * (scan_np(N) + 4));
-}
-
-// Stage state elements [n0, n0 + width) of B and C of the chunk's tokens as fp32
-// (zeros behind the sequence's end and past N).
+// Shared memory.  Two buffers of what arrives while the step before is computed
+// (U, delta, Z of a chunk; 16 state elements of B and C: fp32 lands in its final
+// place, bf16 is widened into one more tile), two buffers of the spans' end states
+// and decays, the state and A log2(e) of the CTA's channels.
 template <typename T_>
-__device__ __forceinline__ void scan_stage(float* tile, const T_* src, long long ld, int tokens,
-                                           int N, int n0, int width) {
-  const int span = kScanK * width + 4;
-  constexpr int V = 16 / sizeof(T_);
-  const bool vec = (reinterpret_cast<uintptr_t>(src) & 15) == 0 && ld % V == 0 && N % V == 0 &&
-                   n0 % V == 0 && width % V == 0;
-  if (vec) {
-    const int per_row = width / V;
-    for (int e = threadIdx.x; e < kScanChunk * per_row; e += kScanThreads) {
-      const int t = e / per_row, i = (e - t * per_row) * V;
-      float v[V];
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (t < tokens && n0 + i < N) raw = __ldg(reinterpret_cast<const uint4*>(src + t * ld + n0 + i));
-      const T_* p = reinterpret_cast<const T_*>(&raw);
+struct ScanShape {
+  static constexpr bool WIDEN = sizeof(T_) == 2;
+  static constexpr int RAW = 2 * 3 * kRawTile * int(sizeof(T_));
+  static constexpr int BC = 2 * 2 * (WIDEN ? kSlabRaw * 2 : kSlabTile * 4);
+  static constexpr int TILES = WIDEN ? 2 * kSlabTile * 4 : 0;
+  static constexpr int ENDS = 2 * 2 * kScanThreads * 16;
+};
+__host__ __device__ constexpr int scan_np(int N) { return (N + 3) & ~3; }
+template <typename T_>
+__host__ __device__ constexpr int scan_smem_bytes(int N) {
+  using S = ScanShape<T_>;
+  return S::RAW + S::BC + S::TILES + S::ENDS + 2 * kScanCh * (scan_np(N) + 4) * 4;
+}
+
+// 16 bytes global -> shared, not waited for; zeros where valid is false.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// What the copies of one operand may assume: 16-byte pieces of its rows.
+template <typename T_>
+__device__ __forceinline__ bool pieces_ok(const T_* p, long long ld, int unit) {
+  constexpr int V = 16 / int(sizeof(T_));
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % V == 0 && unit % V == 0;
+}
+
+// [tokens][nch] of one of U, delta, Z into a raw tile (zeros elsewhere).
+template <typename T_>
+__device__ __forceinline__ void fetch_rows(T_* tile, const T_* src, long long ld, int tokens, int nch,
+                                           bool pieces) {
+  constexpr int V = 16 / int(sizeof(T_));
+  if (pieces) {
+    constexpr int P = kScanCh / V;
+    static_assert(kScanChunk * P % kScanThreads == 0, "whole passes");
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = to_f32(p[j]);
-      float* dst = tile + (t / kScanK) * span + (t % kScanK) * width + i;
-#pragma unroll
-      for (int j = 0; j < V; j += 4)
-        *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    for (int i = 0; i < kScanChunk * P / kScanThreads; ++i) {
+      const int e = i * kScanThreads + static_cast<int>(threadIdx.x);
+      const int t = e / P, c = (e % P) * V;
+      const bool in = t < tokens && c < nch;
+      copy16_async(tile + (t / kScanK) * kRawSpan + (t % kScanK) * kScanCh + c,
+                   src + (in ? t * ld + c : 0), in);
     }
   } else {
-    for (int e = threadIdx.x; e < kScanChunk * width; e += kScanThreads) {
-      const int t = e / width, i = e - t * width;
-      tile[(t / kScanK) * span + (t % kScanK) * width + i] =
-          (t < tokens && n0 + i < N) ? to_f32(src[t * ld + n0 + i]) : 0.f;
+    for (int e = threadIdx.x; e < kScanChunk * kScanCh; e += kScanThreads) {
+      const int t = e / kScanCh, c = e % kScanCh;
+      tile[(t / kScanK) * kRawSpan + (t % kScanK) * kScanCh + c] =
+          (t < tokens && c < nch) ? src[t * ld + c] : from_f32<T_>(0.f);
     }
   }
 }
+
+// State elements [n0, n0 + 16) of B or C of a chunk's tokens (zeros behind the
+// end and past N): fp32 into its final tile, bf16 as it is.
+template <typename T_>
+__device__ __forceinline__ void fetch_slab(T_* dst, const T_* src, long long ld, int tokens, int N,
+                                           int n0, bool pieces) {
+  constexpr int V = 16 / int(sizeof(T_)), P = kScanSlab / V;
+  constexpr bool WIDEN = ScanShape<T_>::WIDEN;
+  auto place = [](int t, int n) {
+    return WIDEN ? t * kScanSlab + n : (t / kScanK) * kSlabSpan + (t % kScanK) * kScanSlab + n;
+  };
+  if (pieces) {
+#pragma unroll
+    for (int i = 0; i < kScanChunk * P / kScanThreads; ++i) {
+      const int e = i * kScanThreads + static_cast<int>(threadIdx.x);
+      const int t = e / P, n = (e % P) * V;
+      const bool in = t < tokens && n0 + n < N;
+      copy16_async(dst + place(t, n), src + (in ? t * ld + n0 + n : 0), in);
+    }
+  } else {
+    for (int e = threadIdx.x; e < kSlabRaw; e += kScanThreads) {
+      const int t = e / kScanSlab, n = e % kScanSlab;
+      dst[place(t, n)] = (t < tokens && n0 + n < N) ? src[t * ld + n0 + n] : from_f32<T_>(0.f);
+    }
+  }
+}
+
+// bf16 B or C into its fp32 tile: eight elements a thread.
+__device__ __forceinline__ void widen_slab(float* tile, const __nv_bfloat16* raw) {
+  static_assert(kSlabRaw == 8 * kScanThreads, "eight elements a thread");
+  const int e = threadIdx.x * 8, t = e / kScanSlab, n = e % kScanSlab;
+  const uint4 v = *reinterpret_cast<const uint4*>(raw + e);
+  float4* dst = reinterpret_cast<float4*>(tile + (t / kScanK) * kSlabSpan + (t % kScanK) * kScanSlab + n);
+  dst[0] = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  dst[1] = make_float4(__uint_as_float(v.z << 16), __uint_as_float(v.z & 0xffff0000u),
+                       __uint_as_float(v.w << 16), __uint_as_float(v.w & 0xffff0000u));
+}
+__device__ __forceinline__ void widen_slab(float*, const float*) {}
 
 // STATE_ONLY: the first of the two passes of a call that is split over time: every
 // run from a zero state, its end state and sum of steps written, no outputs.
 template <typename T_, bool STATE_ONLY>
 __global__ void __launch_bounds__(kScanThreads, 2)
     scan_chunk_kernel(const ScanArgs<T_> a, const ScanPlan pl, unsigned long long wait_ns) {
-  extern __shared__ __align__(16) float scan_smem[];
-  const int NP = scan_np(a.N), slab_w = min(NP, kScanSlab);
-  const int tile = scan_tile_floats(a.N);
-  float* Bs = scan_smem;
-  float* Cs = Bs + tile;
-  float4* ends = reinterpret_cast<float4*>(Cs + tile);      // [2][segs][ch], end states, then starts
-  float4* decays = ends + 2 * kScanThreads;                 // [2][segs][ch]
+  using S = ScanShape<T_>;
+  extern __shared__ __align__(16) uint8_t scan_smem[];
+  const int NP = scan_np(a.N);
+  T_* raw = reinterpret_cast<T_*>(scan_smem);                       // [2][3][kRawTile]
+  T_* bc = reinterpret_cast<T_*>(scan_smem + S::RAW);               // [2][2][one slab]
+  constexpr int kBc = S::WIDEN ? kSlabRaw : kSlabTile;
+  float* tiles = reinterpret_cast<float*>(scan_smem + S::RAW + S::BC);
+  float4* ends = reinterpret_cast<float4*>(scan_smem + S::RAW + S::BC + S::TILES);
+  float4* decays = ends + 2 * kScanThreads;                         // both [2][segs][ch]
   float* state = reinterpret_cast<float*>(decays + 2 * kScanThreads);  // [ch][NP + 4]
   float* A2s = state + kScanCh * (NP + 4);
   __shared__ int next_task, aborted;
 
   const int tid = threadIdx.x;
   const int ch = tid & 15, seg = tid >> 4;
-  const int span = kScanK * slab_w + 4;
   const int groups = a.B * pl.blocks;
   const int tasks = groups * (STATE_ONLY ? pl.runs - 1 : pl.runs);
+  const int dg = a.d / a.G;
+  const bool pieces_u = pieces_ok(a.U, a.ldu, dg);
+  const bool pieces_t = pieces_ok(a.delta, a.ldt, dg);
+  const bool pieces_z = pieces_ok(a.Z, a.ldz, dg);
+  const bool pieces_b = pieces_ok(a.Bm, a.ldb, a.N), pieces_c = pieces_ok(a.Cm, a.ldc, a.N);
   if (tid == 0) aborted = 0;
   grid_dependency_wait();
 
@@ -264,7 +352,6 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     const int run = task / groups, gb = task - run * groups;
     const int b = gb / pl.blocks, blk = gb - b * pl.blocks;
     const int g = blk / pl.per_group;
-    const int dg = a.d / a.G;
     const int in_group = (blk - g * pl.per_group) * kScanCh;
     const int c0 = g * dg + in_group;
     const int nch = min(kScanCh, dg - in_group);
@@ -284,13 +371,37 @@ __global__ void __launch_bounds__(kScanThreads, 2)
       continue;
     }
 
+    const long long row0 = (long long)b * a.T;
+    // the copies of one step: a chunk's rows with its first slab, or a further slab
+    auto fetch = [&](int t0, int n0, int rows_buf, int bc_buf) {
+      const int tokens = min(kScanChunk, t_end - t0);
+      const long long row = row0 + t0;
+      if (n0 == 0) {
+        T_* r = raw + rows_buf * 3 * kRawTile;
+        fetch_rows(r, a.U + row * a.ldu + c0, a.ldu, tokens, nch, pieces_u);
+        fetch_rows(r + kRawTile, a.delta + row * a.ldt + c0, a.ldt, tokens, nch, pieces_t);
+        if (!STATE_ONLY && a.Z)
+          fetch_rows(r + 2 * kRawTile, a.Z + row * a.ldz + c0, a.ldz, tokens, nch, pieces_z);
+      }
+      T_* dst = bc + bc_buf * 2 * kBc;
+      const long long gn = (long long)g * a.N;
+      fetch_slab(dst, a.Bm + row * a.ldb + gn, a.ldb, tokens, a.N, n0, pieces_b);
+      if (!STATE_ONLY)
+        fetch_slab(dst + kBc, a.Cm + row * a.ldc + gn, a.ldc, tokens, a.N, n0, pieces_c);
+      copy_commit();
+    };
+    if (t_begin < t_end) fetch(t_begin, 0, 0, 0);
+
     if (!STATE_ONLY && pl.chained && !first) {
       if (tid == 0) {
         const WaitCtl wc{&aborted, wait_ns};
         flag_wait_geq(pl.flags + 1 + gb, static_cast<uint32_t>(run), wc);
       }
       __syncthreads();
-      if (*const_cast<volatile int*>(&aborted)) return;
+      if (*const_cast<volatile int*>(&aborted)) {
+        copy_wait_all();
+        return;
+      }
     }
     for (int e = tid; e < kScanCh * NP; e += kScanThreads) {
       const int i = e / NP, n = e - i * NP;
@@ -311,74 +422,71 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
     const float skip = a.D ? a.D[c] : 0.f;
     float steps_total = 0.f;  // STATE_ONLY: this thread's share of the run's sum of s
-    const long long row0 = (long long)b * a.T;
+    int rows_buf = 0, bc_buf = 0;
 
-    for (int t0 = t_begin; t0 < t_end; t0 += kScanChunk) {
+    for (int t0 = t_begin; t0 < t_end; t0 += kScanChunk, rows_buf ^= 1) {
       const int tokens = min(kScanChunk, t_end - t0);
       const int mine0 = seg * kScanK;  // this thread's first token of the chunk
-      const long long row = row0 + t0 + mine0;
       f32x2 s2[kScanK], su2[kScanK], y2[kScanK];
       float sum = 0.f;
-      {
-        float u[kScanK], s[kScanK];
-        const T_* up = a.U + row * a.ldu + c;
-        const T_* sp = a.delta + row * a.ldt + c;
-#pragma unroll
-        for (int k = 0; k < kScanK; ++k) {
-          const bool in = mine0 + k < tokens;
-          u[k] = in ? to_f32(up[k * a.ldu]) : 0.f;
-          s[k] = in ? to_f32(sp[k * a.ldt]) + bias : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < kScanK; ++k) {
-          if (a.softplus) s[k] = mine0 + k < tokens ? softplus_f32(s[k]) : 0.f;
-          sum += s[k];
-          s2[k] = pack2(s[k], s[k]);
-          const float su = s[k] * u[k];
-          su2[k] = pack2(su, su);
-          if (!STATE_ONLY) y2[k] = pack2(skip * u[k], 0.f);
-        }
-        if (!a.D && !STATE_ONLY) {  // no 0 * inf where there is no skip
-#pragma unroll
-          for (int k = 0; k < kScanK; ++k) y2[k] = pack2(0.f, 0.f);
-        }
-      }
-      if (STATE_ONLY) steps_total += sum;
+      const T_* rows = raw + rows_buf * 3 * kRawTile + seg * kRawSpan + ch;
 
-      for (int n0 = 0; n0 < NP; n0 += slab_w) {
-        __syncthreads();  // the tiles' readers of the chunk (or slab) before are done
-        const long long bc_row = row0 + t0;
-        scan_stage(Bs, a.Bm + bc_row * a.ldb + (long long)g * a.N, a.ldb, tokens, a.N, n0, slab_w);
-        if (!STATE_ONLY)
-          scan_stage(Cs, a.Cm + bc_row * a.ldc + (long long)g * a.N, a.ldc, tokens, a.N, n0, slab_w);
-        __syncthreads();
-        const int blocks = min(slab_w, NP - n0) >> 2;
+      for (int n0 = 0; n0 < NP; n0 += kScanSlab, bc_buf ^= 1) {
+        copy_wait_all();
+        __syncthreads();  // this step's copies are in; the readers of the step before are done
+        if (n0 + kScanSlab < NP) fetch(t0, n0 + kScanSlab, rows_buf, bc_buf ^ 1);
+        else if (t0 + kScanChunk < t_end) fetch(t0 + kScanChunk, 0, rows_buf ^ 1, bc_buf ^ 1);
+        const float *Bs, *Cs;
+        if (S::WIDEN) {
+          widen_slab(tiles, bc + bc_buf * 2 * kBc);
+          if (!STATE_ONLY) widen_slab(tiles + kSlabTile, bc + (bc_buf * 2 + 1) * kBc);
+          Bs = tiles;
+        } else {
+          Bs = reinterpret_cast<const float*>(bc + bc_buf * 2 * kBc);
+        }
+        Cs = Bs + kSlabTile;
+        if (n0 == 0) {
+#pragma unroll
+          for (int k = 0; k < kScanK; ++k) {
+            const float u = to_f32(rows[k * kScanCh]);
+            float s = to_f32(rows[kRawTile + k * kScanCh]) + bias;
+            if (a.softplus) s = softplus_f32(s);
+            if (mine0 + k >= tokens) s = 0.f;  // behind the end: the state passes unchanged
+            sum += s;
+            s2[k] = pack2(s, s);
+            const float su = s * u;
+            su2[k] = pack2(su, su);
+            y2[k] = pack2(a.D ? skip * u : 0.f, 0.f);  // no 0 * inf where there is no skip
+          }
+          if (STATE_ONLY) steps_total += sum;
+        }
+        if (S::WIDEN) __syncthreads();
+        const int blocks = min(kScanSlab, NP - n0) >> 2;
 #pragma unroll 1
         for (int nb = 0; nb < blocks; ++nb) {
           const int buf = (nb & 1) * kScanThreads;
           const float4 A4 = *reinterpret_cast<const float4*>(A2s + ch * (NP + 4) + n0 + nb * 4);
           const f32x2 A01 = pack2(A4.x, A4.y), A23 = pack2(A4.z, A4.w);
-          const float* bp = Bs + seg * span + nb * 4;
+          const float* bp = Bs + seg * kSlabSpan + nb * 4;
           f32x2 a01[kScanK], a23[kScanK];
           f32x2 h01 = 0ull, h23 = 0ull;
 #pragma unroll
           for (int k = 0; k < kScanK; ++k) {
-            const float4 b4 = *reinterpret_cast<const float4*>(bp + k * slab_w);
+            const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(bp + k * kScanSlab);
             float x0, x1, x2, x3;
             unpack2(mul2(s2[k], A01), x0, x1);
             unpack2(mul2(s2[k], A23), x2, x3);
             a01[k] = pack2(exp2_approx(x0), exp2_approx(x1));
             a23[k] = pack2(exp2_approx(x2), exp2_approx(x3));
-            h01 = fma2(a01[k], h01, mul2(su2[k], pack2(b4.x, b4.y)));
-            h23 = fma2(a23[k], h23, mul2(su2[k], pack2(b4.z, b4.w)));
+            h01 = fma2(a01[k], h01, mul2(su2[k], b4.x));
+            h23 = fma2(a23[k], h23, mul2(su2[k], b4.y));
           }
           float4 e4;
           unpack2(h01, e4.x, e4.y);
           unpack2(h23, e4.z, e4.w);
-          ends[buf + seg * kScanCh + ch] = e4;
-          decays[buf + seg * kScanCh + ch] =
-              make_float4(exp2_approx(sum * A4.x), exp2_approx(sum * A4.y), exp2_approx(sum * A4.z),
-                          exp2_approx(sum * A4.w));
+          ends[buf + tid] = e4;
+          decays[buf + tid] = make_float4(exp2_approx(sum * A4.x), exp2_approx(sum * A4.y),
+                                          exp2_approx(sum * A4.z), exp2_approx(sum * A4.w));
           __syncthreads();
           if (tid < kScanCh * 4) {
             // one state element of one channel: the spans in order
@@ -396,33 +504,32 @@ __global__ void __launch_bounds__(kScanThreads, 2)
           }
           if (STATE_ONLY) continue;  // two buffers: the next block writes the other one
           __syncthreads();
-          const float4 start = ends[buf + seg * kScanCh + ch];
-          h01 = pack2(start.x, start.y);
-          h23 = pack2(start.z, start.w);
-          const float* cp = Cs + seg * span + nb * 4;
+          const ulonglong2 start = *reinterpret_cast<const ulonglong2*>(ends + buf + tid);
+          h01 = start.x;
+          h23 = start.y;
+          const float* cp = Cs + seg * kSlabSpan + nb * 4;
 #pragma unroll
           for (int k = 0; k < kScanK; ++k) {
-            const float4 b4 = *reinterpret_cast<const float4*>(bp + k * slab_w);
-            const float4 c4 = *reinterpret_cast<const float4*>(cp + k * slab_w);
-            h01 = fma2(a01[k], h01, mul2(su2[k], pack2(b4.x, b4.y)));
-            h23 = fma2(a23[k], h23, mul2(su2[k], pack2(b4.z, b4.w)));
-            y2[k] = fma2(h01, pack2(c4.x, c4.y), y2[k]);
-            y2[k] = fma2(h23, pack2(c4.z, c4.w), y2[k]);
+            const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(bp + k * kScanSlab);
+            const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(cp + k * kScanSlab);
+            h01 = fma2(a01[k], h01, mul2(su2[k], b4.x));
+            h23 = fma2(a23[k], h23, mul2(su2[k], b4.y));
+            y2[k] = fma2(h01, c4.x, y2[k]);
+            y2[k] = fma2(h23, c4.y, y2[k]);
           }
         }
       }
 
       if (!STATE_ONLY && mine) {
-        T_* yp = a.Y + row * a.ldy + c;
-        const T_* zp = a.Z ? a.Z + row * a.ldz + c : nullptr;
+        T_* yp = a.Y + (row0 + t0 + mine0) * a.ldy + c;
 #pragma unroll
-        for (int k = 0; k < kScanK; ++k) {
+        for (int k = 0; k < kScanK; ++k, yp += a.ldy) {
           if (mine0 + k < tokens) {
             float lo, hi;
             unpack2(y2[k], lo, hi);
             float y = lo + hi;
-            if (zp) y *= activate(to_f32(zp[k * a.ldz]), ITTT_ACT_SILU);
-            yp[k * a.ldy] = from_f32<T_>(y);
+            if (a.Z) y *= silu_gate(to_f32(rows[2 * kRawTile + k * kScanCh]));
+            *yp = from_f32<T_>(y);
           }
         }
       }
