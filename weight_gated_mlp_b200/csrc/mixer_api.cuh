@@ -304,10 +304,10 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   const long long chunks = cdiv(p->T, kScanChunk);
   long long run_chunks = chunks;
   if (groups * 4 >= workers * 3) {
-    // enough channel blocks for every CTA: runs of 8 chunks, chained, so that the
+    // enough channel blocks for every CTA: runs of 4 chunks, chained, so that the
     // work is dealt out evenly however many blocks there are
     c.chained = true;
-    if (groups < 6 * workers) run_chunks = std::min(chunks, 8ll);
+    if (groups < 6 * workers) run_chunks = std::min(chunks, 4ll);
   } else {
     // few channels: independent runs, two tasks for every CTA, a run of at least two chunks
     const long long want = std::max(1ll, 2 * workers / groups);

@@ -7,15 +7,16 @@
 //
 //   scan_serial_kernel  short calls and single tokens: lanes over the state, four
 //       or eight elements a lane, token after token.  Bound by the state's bytes.
-//   scan_chunk_kernel   prompts: 16 channels a CTA, 128 tokens at a time.  A
-//       thread owns one channel and 8 consecutive tokens; for four state elements
-//       at once it runs the recurrence from zero over its tokens, keeping the
-//       exponentials, the CTA joins the 16 spans (a span's decay is
-//       exp(A sum s), one exponential and one rounding for 8 tokens), and the
-//       thread runs its tokens again from the true state, with the kept
-//       exponentials, into y.  The lanes of a half warp are neighbouring channels,
-//       so a row of U, delta, Z and Y is read in whole 32-byte sectors, and B and C
-//       come from shared memory as broadcasts of four state elements.
+//   scan_chunk_kernel   prompts: 16 channels a CTA, 256 tokens at a time.  A
+//       thread owns two neighbouring channels and 8 consecutive tokens, a warp two
+//       channels and the whole chunk.  For two state elements at once a thread runs
+//       the recurrence from zero over its tokens and keeps the exponentials; the
+//       warp joins its 32 spans (a span's decay is exp(A sum s): one exponential
+//       and one rounding for 8 tokens); the thread runs its tokens again from the
+//       true state, with the kept exponentials, into y.  Two channels a thread halve
+//       what a state element costs in shared-memory reads of B and C (32 words a
+//       clock and SM, however many lanes read the same word), and the joins stay
+//       inside a warp, so the CTA meets four times a chunk only.
 #pragma once
 
 #include "common.cuh"
@@ -177,12 +178,10 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, 
 
 // ---------------------------------------------------------------- prompts
 
-constexpr int kScanCh = 16;                       // channels a CTA
-constexpr int kScanSegs = 16;                     // spans of a chunk
-constexpr int kScanK = 8;                         // tokens a span
-constexpr int kScanChunk = kScanSegs * kScanK;    // tokens a chunk
-constexpr int kScanThreads = kScanCh * kScanSegs;
-constexpr int kScanSlab = 16;                     // state elements of B and C staged at once
+constexpr int kScanThreads = 256;
+constexpr int kScanCh = 16;                       // channels a CTA, two a warp
+constexpr int kScanK = 8;                         // tokens a span, one span a lane
+constexpr int kScanChunk = 32 * kScanK;           // tokens a chunk
 
 // How the work of a call is cut.  A task is one channel block of one sequence
 // over one run of tokens; tasks are handed out run by run.
@@ -193,37 +192,35 @@ struct ScanPlan {
   int run_tokens;  // a multiple of kScanChunk
   int chained;     // 1: a run starts from the state that the run before leaves in
                    // `carry`; 0: run r from carry[r - 1] (filled by scan_join_kernel)
-  float* carry;    // chained: [B blocks][16][NP]; else [runs - 1][B, d, N]
+  float* carry;    // chained: [B blocks][16 NP]; else [runs - 1][B, d, N]
   float* step_sum; // state pass: [runs - 1][B, d], the runs' sums of s
   unsigned* flags; // chained: [0] the next task, [1 + B blocks] runs finished
 };
 
-// Rows of the staged tiles: a span's 8 tokens side by side, the spans 16 (raw
-// rows) or 4 (B and C in fp32) elements further apart than that, so that the two
-// spans of a warp read different banks.
-constexpr int kRawSpan = kScanK * kScanCh + 16;
-constexpr int kRawTile = kScanSegs * kRawSpan;        // elements of one of U, delta, Z
-constexpr int kSlabSpan = kScanK * kScanSlab + 4;
-constexpr int kSlabTile = kScanSegs * kSlabSpan;      // fp32 elements of one of B, C
-constexpr int kSlabRaw = kScanChunk * kScanSlab;      // bf16 elements of one of B, C
-
-// Shared memory.  Two buffers of what arrives while the step before is computed
-// (U, delta, Z of a chunk; 16 state elements of B and C: fp32 lands in its final
-// place, bf16 is widened into one more tile), two buffers of the spans' end states
-// and decays, the state and A log2(e) of the CTA's channels.
+// A slab: the 32 bytes of state elements of B and C that are staged at once (16
+// bf16, 8 fp32).  Staged rows arrive as they are; B and C are then laid out as
+// [pair of state elements][span][token], so that a lane reads the pair of 4 (or 2)
+// tokens with one 16-byte load; the spans stand 12 (20) words apart, which puts the
+// eight lanes of a quarter warp on different banks.
 template <typename T_>
 struct ScanShape {
-  static constexpr bool WIDEN = sizeof(T_) == 2;
-  static constexpr int RAW = 2 * 3 * kRawTile * int(sizeof(T_));
-  static constexpr int BC = 2 * 2 * (WIDEN ? kSlabRaw * 2 : kSlabTile * 4);
-  static constexpr int TILES = WIDEN ? 2 * kSlabTile * 4 : 0;
-  static constexpr int ENDS = 2 * 2 * kScanThreads * 16;
+  static constexpr int ES = int(sizeof(T_));
+  static constexpr int SLAB = 32 / ES;                       // state elements
+  static constexpr int PAIRS = SLAB / 2;
+  static constexpr int ROW_SPAN = kScanK * kScanCh + 16 / ES;  // elements between spans of raw rows
+  static constexpr int ROW_TILE = 32 * ROW_SPAN;
+  static constexpr int PAIR_SPAN = kScanK * 2 * ES / 4 + 4;  // words between spans of laid out pairs
+  static constexpr int PAIR_TILE = 32 * PAIR_SPAN;           // words of one pair
+  static constexpr int ROWS = 3 * ROW_TILE * ES;             // bytes: U, delta, Z (and Y)
+  static constexpr int RAW = 2 * kScanChunk * 32;            // bytes: B and C as they come
+  static constexpr int TILES = 2 * PAIRS * PAIR_TILE * 4;    // bytes: B and C laid out
 };
-__host__ __device__ constexpr int scan_np(int N) { return (N + 3) & ~3; }
+constexpr int kEndsWarp = 32 * 4 + 8 * 4;  // a warp's end states: 4 floats a span, 4 more every 4 spans
+__host__ __device__ constexpr int scan_np(int N) { return (N + 1) & ~1; }
 template <typename T_>
 __host__ __device__ constexpr int scan_smem_bytes(int N) {
   using S = ScanShape<T_>;
-  return S::RAW + S::BC + S::TILES + S::ENDS + 2 * kScanCh * (scan_np(N) + 4) * 4;
+  return S::ROWS + S::RAW + S::TILES + 8 * kEndsWarp * 4 + 2 * kScanCh * scan_np(N) * 4;
 }
 
 // 16 bytes global -> shared, not waited for; zeros where valid is false.
@@ -233,7 +230,11 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src, bool va
                : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// Wait until at most N of this thread's committed groups are still on their way.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // What the copies of one operand may assume: 16-byte pieces of its rows.
 template <typename T_>
@@ -242,69 +243,135 @@ __device__ __forceinline__ bool pieces_ok(const T_* p, long long ld, int unit) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % V == 0 && unit % V == 0;
 }
 
-// [tokens][nch] of one of U, delta, Z into a raw tile (zeros elsewhere).
+// [tokens][nch] of one of U, delta, Z into a tile of rows (zeros elsewhere).
 template <typename T_>
 __device__ __forceinline__ void fetch_rows(T_* tile, const T_* src, long long ld, int tokens, int nch,
                                            bool pieces) {
-  constexpr int V = 16 / int(sizeof(T_));
+  using S = ScanShape<T_>;
+  constexpr int V = 16 / S::ES, P = kScanCh / V;
   if (pieces) {
-    constexpr int P = kScanCh / V;
-    static_assert(kScanChunk * P % kScanThreads == 0, "whole passes");
 #pragma unroll
     for (int i = 0; i < kScanChunk * P / kScanThreads; ++i) {
       const int e = i * kScanThreads + static_cast<int>(threadIdx.x);
       const int t = e / P, c = (e % P) * V;
       const bool in = t < tokens && c < nch;
-      copy16_async(tile + (t / kScanK) * kRawSpan + (t % kScanK) * kScanCh + c,
+      copy16_async(tile + (t / kScanK) * S::ROW_SPAN + (t % kScanK) * kScanCh + c,
                    src + (in ? t * ld + c : 0), in);
     }
   } else {
     for (int e = threadIdx.x; e < kScanChunk * kScanCh; e += kScanThreads) {
       const int t = e / kScanCh, c = e % kScanCh;
-      tile[(t / kScanK) * kRawSpan + (t % kScanK) * kScanCh + c] =
+      tile[(t / kScanK) * S::ROW_SPAN + (t % kScanK) * kScanCh + c] =
           (t < tokens && c < nch) ? src[t * ld + c] : from_f32<T_>(0.f);
     }
   }
 }
 
-// State elements [n0, n0 + 16) of B or C of a chunk's tokens (zeros behind the
-// end and past N): fp32 into its final tile, bf16 as it is.
+// A tile of rows to Y: the counterpart of fetch_rows.
 template <typename T_>
-__device__ __forceinline__ void fetch_slab(T_* dst, const T_* src, long long ld, int tokens, int N,
-                                           int n0, bool pieces) {
-  constexpr int V = 16 / int(sizeof(T_)), P = kScanSlab / V;
-  constexpr bool WIDEN = ScanShape<T_>::WIDEN;
-  auto place = [](int t, int n) {
-    return WIDEN ? t * kScanSlab + n : (t / kScanK) * kSlabSpan + (t % kScanK) * kScanSlab + n;
-  };
+__device__ __forceinline__ void store_rows(T_* dst, const T_* tile, long long ld, int tokens, int nch,
+                                           bool pieces) {
+  using S = ScanShape<T_>;
+  constexpr int V = 16 / S::ES, P = kScanCh / V;
   if (pieces) {
 #pragma unroll
     for (int i = 0; i < kScanChunk * P / kScanThreads; ++i) {
       const int e = i * kScanThreads + static_cast<int>(threadIdx.x);
-      const int t = e / P, n = (e % P) * V;
-      const bool in = t < tokens && n0 + n < N;
-      copy16_async(dst + place(t, n), src + (in ? t * ld + n0 + n : 0), in);
+      const int t = e / P, c = (e % P) * V;
+      if (t < tokens && c < nch)
+        *reinterpret_cast<uint4*>(dst + t * ld + c) = *reinterpret_cast<const uint4*>(
+            tile + (t / kScanK) * S::ROW_SPAN + (t % kScanK) * kScanCh + c);
     }
   } else {
-    for (int e = threadIdx.x; e < kSlabRaw; e += kScanThreads) {
-      const int t = e / kScanSlab, n = e % kScanSlab;
-      dst[place(t, n)] = (t < tokens && n0 + n < N) ? src[t * ld + n0 + n] : from_f32<T_>(0.f);
+    for (int e = threadIdx.x; e < kScanChunk * kScanCh; e += kScanThreads) {
+      const int t = e / kScanCh, c = e % kScanCh;
+      if (t < tokens && c < nch)
+        dst[t * ld + c] = tile[(t / kScanK) * S::ROW_SPAN + (t % kScanK) * kScanCh + c];
     }
   }
 }
 
-// bf16 B or C into its fp32 tile: eight elements a thread.
-__device__ __forceinline__ void widen_slab(float* tile, const __nv_bfloat16* raw) {
-  static_assert(kSlabRaw == 8 * kScanThreads, "eight elements a thread");
-  const int e = threadIdx.x * 8, t = e / kScanSlab, n = e % kScanSlab;
-  const uint4 v = *reinterpret_cast<const uint4*>(raw + e);
-  float4* dst = reinterpret_cast<float4*>(tile + (t / kScanK) * kSlabSpan + (t % kScanK) * kScanSlab + n);
-  dst[0] = make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
-  dst[1] = make_float4(__uint_as_float(v.z << 16), __uint_as_float(v.z & 0xffff0000u),
-                       __uint_as_float(v.w << 16), __uint_as_float(v.w & 0xffff0000u));
+// The slab [n0, n0 + SLAB) of B or C of a chunk's tokens, as it comes: [token][SLAB]
+// (zeros behind the end and past N).
+template <typename T_>
+__device__ __forceinline__ void fetch_slab(T_* dst, const T_* src, long long ld, int tokens, int N,
+                                           int n0, bool pieces) {
+  using S = ScanShape<T_>;
+  constexpr int V = 16 / S::ES;
+  if (pieces) {
+#pragma unroll
+    for (int i = 0; i < 2 * kScanChunk / kScanThreads; ++i) {
+      const int e = i * kScanThreads + static_cast<int>(threadIdx.x);
+      const int t = e >> 1, n = (e & 1) * V;
+      const bool in = t < tokens && n0 + n < N;
+      copy16_async(dst + t * S::SLAB + n, src + (in ? t * ld + n0 + n : 0), in);
+    }
+  } else {
+    for (int e = threadIdx.x; e < kScanChunk * S::SLAB; e += kScanThreads) {
+      const int t = e / S::SLAB, n = e % S::SLAB;
+      dst[e] = (t < tokens && n0 + n < N) ? src[t * ld + n0 + n] : from_f32<T_>(0.f);
+    }
+  }
 }
-__device__ __forceinline__ void widen_slab(float*, const float*) {}
+
+// [token][SLAB] -> [pair][span][token]: one token a thread.
+template <typename T_>
+__device__ __forceinline__ void lay_out(uint32_t* tile, const T_* raw) {
+  using S = ScanShape<T_>;
+  const int t = threadIdx.x;
+  const uint4* src = reinterpret_cast<const uint4*>(raw + t * S::SLAB);
+  const uint4 lo = src[0], hi = src[1];
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t* dst = tile + (t / kScanK) * S::PAIR_SPAN + (t % kScanK) * (S::ES / 2);
+  if (S::ES == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dst[i * S::PAIR_TILE] = w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint2*>(dst + i * S::PAIR_TILE) = make_uint2(w[2 * i], w[2 * i + 1]);
+  }
+}
+
+// One pair's values of a span's eight tokens.
+template <typename T_>
+struct PairSpan;
+template <>
+struct PairSpan<__nv_bfloat16> {
+  uint32_t w[8];
+  __device__ __forceinline__ explicit PairSpan(const uint32_t* p) {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+  __device__ __forceinline__ float lo(int k) const { return __uint_as_float(w[k] << 16); }
+  __device__ __forceinline__ float hi(int k) const { return __uint_as_float(w[k] & 0xffff0000u); }
+};
+template <>
+struct PairSpan<float> {
+  float w[16];
+  __device__ __forceinline__ explicit PairSpan(const uint32_t* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 a = reinterpret_cast<const float4*>(p)[i];
+      w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+    }
+  }
+  __device__ __forceinline__ float lo(int k) const { return w[2 * k]; }
+  __device__ __forceinline__ float hi(int k) const { return w[2 * k + 1]; }
+};
+
+// Two neighbouring channels of a row.
+__device__ __forceinline__ float2 load_two(const __nv_bfloat16* p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 load_two(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ void store_two(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
+}
+__device__ __forceinline__ void store_two(float* p, float x, float y) {
+  *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
 
 // STATE_ONLY: the first of the two passes of a call that is split over time: every
 // run from a zero state, its end state and sum of steps written, no outputs.
@@ -314,25 +381,28 @@ __global__ void __launch_bounds__(kScanThreads, 2)
   using S = ScanShape<T_>;
   extern __shared__ __align__(16) uint8_t scan_smem[];
   const int NP = scan_np(a.N);
-  T_* raw = reinterpret_cast<T_*>(scan_smem);                       // [2][3][kRawTile]
-  T_* bc = reinterpret_cast<T_*>(scan_smem + S::RAW);               // [2][2][one slab]
-  constexpr int kBc = S::WIDEN ? kSlabRaw : kSlabTile;
-  float* tiles = reinterpret_cast<float*>(scan_smem + S::RAW + S::BC);
-  float4* ends = reinterpret_cast<float4*>(scan_smem + S::RAW + S::BC + S::TILES);
-  float4* decays = ends + 2 * kScanThreads;                         // both [2][segs][ch]
-  float* state = reinterpret_cast<float*>(decays + 2 * kScanThreads);  // [ch][NP + 4]
-  float* A2s = state + kScanCh * (NP + 4);
+  T_* rows = reinterpret_cast<T_*>(scan_smem);                        // U, delta, Z (then Y)
+  T_* raw = reinterpret_cast<T_*>(scan_smem + S::ROWS);               // B, C as they come
+  uint32_t* tiles = reinterpret_cast<uint32_t*>(scan_smem + S::ROWS + S::RAW);
+  float* ends_all = reinterpret_cast<float*>(scan_smem + S::ROWS + S::RAW + S::TILES);
+  float* state = ends_all + 8 * kEndsWarp;                            // [ch][NP]
+  float* A2s = state + kScanCh * NP;                                  // [ch][NP], A log2(e)
   __shared__ int next_task, aborted;
 
-  const int tid = threadIdx.x;
-  const int ch = tid & 15, seg = tid >> 4;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int groups = a.B * pl.blocks;
   const int tasks = groups * (STATE_ONLY ? pl.runs - 1 : pl.runs);
   const int dg = a.d / a.G;
-  const bool pieces_u = pieces_ok(a.U, a.ldu, dg);
-  const bool pieces_t = pieces_ok(a.delta, a.ldt, dg);
-  const bool pieces_z = pieces_ok(a.Z, a.ldz, dg);
+  const bool pieces_u = pieces_ok(a.U, a.ldu, dg), pieces_t = pieces_ok(a.delta, a.ldt, dg);
+  const bool pieces_z = pieces_ok(a.Z, a.ldz, dg), pieces_y = pieces_ok(a.Y, a.ldy, dg);
   const bool pieces_b = pieces_ok(a.Bm, a.ldb, a.N), pieces_c = pieces_ok(a.Cm, a.ldc, a.N);
+  // joins: lane -> one state element of one channel (q = 2 element + channel) and 4 spans
+  float* ends = ends_all + warp * kEndsWarp;
+  float* my_end = ends + lane * 4 + (lane >> 2) * 4;
+  const int q = lane & 3, first_span = (lane >> 2) * 4;
+  float* join_ends = ends + first_span * 4 + (first_span >> 2) * 4 + q;
+  const float* join_state = state + (2 * warp + (q & 1)) * NP + (q >> 1);
+  const float* join_A2 = A2s + (2 * warp + (q & 1)) * NP + (q >> 1);
   if (tid == 0) aborted = 0;
   grid_dependency_wait();
 
@@ -355,8 +425,6 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     const int in_group = (blk - g * pl.per_group) * kScanCh;
     const int c0 = g * dg + in_group;
     const int nch = min(kScanCh, dg - in_group);
-    const bool mine = ch < nch;
-    const int c = c0 + (mine ? ch : 0);
     const int len = sequence_length(a.lengths, b, a.T);
     const int t_begin = run * pl.run_tokens;
     const int t_end = min(len, t_begin + pl.run_tokens);
@@ -372,25 +440,24 @@ __global__ void __launch_bounds__(kScanThreads, 2)
     }
 
     const long long row0 = (long long)b * a.T;
-    // the copies of one step: a chunk's rows with its first slab, or a further slab
-    auto fetch = [&](int t0, int n0, int rows_buf, int bc_buf) {
+    auto fetch_inputs = [&](int t0) {
       const int tokens = min(kScanChunk, t_end - t0);
       const long long row = row0 + t0;
-      if (n0 == 0) {
-        T_* r = raw + rows_buf * 3 * kRawTile;
-        fetch_rows(r, a.U + row * a.ldu + c0, a.ldu, tokens, nch, pieces_u);
-        fetch_rows(r + kRawTile, a.delta + row * a.ldt + c0, a.ldt, tokens, nch, pieces_t);
-        if (!STATE_ONLY && a.Z)
-          fetch_rows(r + 2 * kRawTile, a.Z + row * a.ldz + c0, a.ldz, tokens, nch, pieces_z);
-      }
-      T_* dst = bc + bc_buf * 2 * kBc;
-      const long long gn = (long long)g * a.N;
-      fetch_slab(dst, a.Bm + row * a.ldb + gn, a.ldb, tokens, a.N, n0, pieces_b);
-      if (!STATE_ONLY)
-        fetch_slab(dst + kBc, a.Cm + row * a.ldc + gn, a.ldc, tokens, a.N, n0, pieces_c);
-      copy_commit();
+      fetch_rows(rows, a.U + row * a.ldu + c0, a.ldu, tokens, nch, pieces_u);
+      fetch_rows(rows + S::ROW_TILE, a.delta + row * a.ldt + c0, a.ldt, tokens, nch, pieces_t);
     };
-    if (t_begin < t_end) fetch(t_begin, 0, 0, 0);
+    auto fetch_bc = [&](int t0, int n0) {
+      const int tokens = min(kScanChunk, t_end - t0);
+      const long long row = row0 + t0, gn = (long long)g * a.N;
+      fetch_slab(raw, a.Bm + row * a.ldb + gn, a.ldb, tokens, a.N, n0, pieces_b);
+      if (!STATE_ONLY)
+        fetch_slab(raw + kScanChunk * S::SLAB, a.Cm + row * a.ldc + gn, a.ldc, tokens, a.N, n0, pieces_c);
+    };
+    if (t_begin < t_end) {
+      fetch_inputs(t_begin);
+      fetch_bc(t_begin, 0);
+      copy_commit();
+    }
 
     if (!STATE_ONLY && pl.chained && !first) {
       if (tid == 0) {
@@ -399,7 +466,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
       }
       __syncthreads();
       if (*const_cast<volatile int*>(&aborted)) {
-        copy_wait_all();
+        copy_wait<0>();
         return;
       }
     }
@@ -415,148 +482,203 @@ __global__ void __launch_bounds__(kScanThreads, 2)
           else h = pl.carry[(long long)(run - 1) * a.B * a.d * a.N + at];
         }
       }
-      state[i * (NP + 4) + n] = h;
-      A2s[i * (NP + 4) + n] = A2;
+      state[e] = h;
+      A2s[e] = A2;
     }
 
-    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
-    const float skip = a.D ? a.D[c] : 0.f;
-    float steps_total = 0.f;  // STATE_ONLY: this thread's share of the run's sum of s
-    int rows_buf = 0, bc_buf = 0;
+    // this thread's two channels (past nch: zeros in, nothing out)
+    const int ch = 2 * warp;
+    float2 bias = make_float2(0.f, 0.f), skip = make_float2(0.f, 0.f);
+    if (a.dt_bias) {
+      if (ch < nch) bias.x = a.dt_bias[c0 + ch];
+      if (ch + 1 < nch) bias.y = a.dt_bias[c0 + ch + 1];
+    }
+    if (a.D) {
+      if (ch < nch) skip.x = a.D[c0 + ch];
+      if (ch + 1 < nch) skip.y = a.D[c0 + ch + 1];
+    }
+    float2 steps_total = make_float2(0.f, 0.f);  // STATE_ONLY: this lane's share of the run's sums of s
+    const T_* my_rows = rows + lane * S::ROW_SPAN + ch;
 
-    for (int t0 = t_begin; t0 < t_end; t0 += kScanChunk, rows_buf ^= 1) {
+    for (int t0 = t_begin; t0 < t_end; t0 += kScanChunk) {
       const int tokens = min(kScanChunk, t_end - t0);
-      const int mine0 = seg * kScanK;  // this thread's first token of the chunk
-      f32x2 s2[kScanK], su2[kScanK], y2[kScanK];
-      float sum = 0.f;
-      const T_* rows = raw + rows_buf * 3 * kRawTile + seg * kRawSpan + ch;
+      const int mine0 = lane * kScanK;  // this thread's first token of the chunk
+      f32x2 s2[kScanK];                 // (channel, next channel)
+      float2 su[kScanK], y[kScanK];
+      float join_sum[4];                // sums of s of the four spans that this lane joins
 
-      for (int n0 = 0; n0 < NP; n0 += kScanSlab, bc_buf ^= 1) {
-        copy_wait_all();
-        __syncthreads();  // this step's copies are in; the readers of the step before are done
-        if (n0 + kScanSlab < NP) fetch(t0, n0 + kScanSlab, rows_buf, bc_buf ^ 1);
-        else if (t0 + kScanChunk < t_end) fetch(t0 + kScanChunk, 0, rows_buf ^ 1, bc_buf ^ 1);
-        const float *Bs, *Cs;
-        if (S::WIDEN) {
-          widen_slab(tiles, bc + bc_buf * 2 * kBc);
-          if (!STATE_ONLY) widen_slab(tiles + kSlabTile, bc + (bc_buf * 2 + 1) * kBc);
-          Bs = tiles;
-        } else {
-          Bs = reinterpret_cast<const float*>(bc + bc_buf * 2 * kBc);
-        }
-        Cs = Bs + kSlabTile;
+      for (int n0 = 0; n0 < NP; n0 += S::SLAB) {
+        copy_wait<0>();
+        __syncthreads();  // the copies are in; the tiles' readers of the step before are done
         if (n0 == 0) {
+          if (!STATE_ONLY && a.Z) {
+            fetch_rows(rows + 2 * S::ROW_TILE, a.Z + (row0 + t0) * a.ldz + c0, a.ldz, tokens, nch, pieces_z);
+            copy_commit();
+          }
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < kScanK; ++k) {
-            const float u = to_f32(rows[k * kScanCh]);
-            float s = to_f32(rows[kRawTile + k * kScanCh]) + bias;
-            if (a.softplus) s = softplus_f32(s);
-            if (mine0 + k >= tokens) s = 0.f;  // behind the end: the state passes unchanged
-            sum += s;
-            s2[k] = pack2(s, s);
-            const float su = s * u;
-            su2[k] = pack2(su, su);
-            y2[k] = pack2(a.D ? skip * u : 0.f, 0.f);  // no 0 * inf where there is no skip
-          }
-          if (STATE_ONLY) steps_total += sum;
-        }
-        if (S::WIDEN) __syncthreads();
-        const int blocks = min(kScanSlab, NP - n0) >> 2;
-#pragma unroll 1
-        for (int nb = 0; nb < blocks; ++nb) {
-          const int buf = (nb & 1) * kScanThreads;
-          const float4 A4 = *reinterpret_cast<const float4*>(A2s + ch * (NP + 4) + n0 + nb * 4);
-          const f32x2 A01 = pack2(A4.x, A4.y), A23 = pack2(A4.z, A4.w);
-          const float* bp = Bs + seg * kSlabSpan + nb * 4;
-          f32x2 a01[kScanK], a23[kScanK];
-          f32x2 h01 = 0ull, h23 = 0ull;
-#pragma unroll
-          for (int k = 0; k < kScanK; ++k) {
-            const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(bp + k * kScanSlab);
-            float x0, x1, x2, x3;
-            unpack2(mul2(s2[k], A01), x0, x1);
-            unpack2(mul2(s2[k], A23), x2, x3);
-            a01[k] = pack2(exp2_approx(x0), exp2_approx(x1));
-            a23[k] = pack2(exp2_approx(x2), exp2_approx(x3));
-            h01 = fma2(a01[k], h01, mul2(su2[k], b4.x));
-            h23 = fma2(a23[k], h23, mul2(su2[k], b4.y));
-          }
-          float4 e4;
-          unpack2(h01, e4.x, e4.y);
-          unpack2(h23, e4.z, e4.w);
-          ends[buf + tid] = e4;
-          decays[buf + tid] = make_float4(exp2_approx(sum * A4.x), exp2_approx(sum * A4.y),
-                                          exp2_approx(sum * A4.z), exp2_approx(sum * A4.w));
-          __syncthreads();
-          if (tid < kScanCh * 4) {
-            // one state element of one channel: the spans in order
-            float* e = reinterpret_cast<float*>(ends + buf) + tid;
-            const float* p = reinterpret_cast<const float*>(decays + buf) + tid;
-            float* st = state + (tid >> 2) * (NP + 4) + n0 + nb * 4 + (tid & 3);
-            float h = *st;
-#pragma unroll
-            for (int i = 0; i < kScanSegs; ++i) {
-              const float end = e[i * kScanCh * 4];
-              if (!STATE_ONLY) e[i * kScanCh * 4] = h;
-              h = fmaf(p[i * kScanCh * 4], h, end);
+            const float2 u = load_two(my_rows + k * kScanCh);
+            float2 s = load_two(my_rows + S::ROW_TILE + k * kScanCh);
+            s.x += bias.x;
+            s.y += bias.y;
+            if (a.softplus) {
+              s.x = softplus_f32(s.x);
+              s.y = softplus_f32(s.y);
             }
-            *st = h;
+            if (mine0 + k >= tokens) s = make_float2(0.f, 0.f);  // behind the end: the state passes
+            sum.x += s.x;
+            sum.y += s.y;
+            s2[k] = pack2(s.x, s.y);
+            su[k] = make_float2(s.x * u.x, s.y * u.y);
+            // no 0 * inf where there is no skip
+            y[k] = a.D ? make_float2(skip.x * u.x, skip.y * u.y) : make_float2(0.f, 0.f);
           }
-          if (STATE_ONLY) continue;  // two buffers: the next block writes the other one
-          __syncthreads();
-          const ulonglong2 start = *reinterpret_cast<const ulonglong2*>(ends + buf + tid);
-          h01 = start.x;
-          h23 = start.y;
-          const float* cp = Cs + seg * kSlabSpan + nb * 4;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = __shfl_sync(0xffffffffu, sum.x, first_span + i);
+            const float z = __shfl_sync(0xffffffffu, sum.y, first_span + i);
+            join_sum[i] = (q & 1) ? z : x;
+          }
+          if (STATE_ONLY) {
+            steps_total.x += sum.x;
+            steps_total.y += sum.y;
+          }
+        }
+        lay_out(tiles, raw);
+        if (!STATE_ONLY) lay_out(tiles + S::PAIRS * S::PAIR_TILE, raw + kScanChunk * S::SLAB);
+        __syncthreads();
+        // what comes next arrives during the recurrences
+        if (n0 + S::SLAB < NP) {
+          fetch_bc(t0, n0 + S::SLAB);
+        } else if (t0 + kScanChunk < t_end) {
+          fetch_inputs(t0 + kScanChunk);
+          fetch_bc(t0 + kScanChunk, 0);
+        }
+        copy_commit();
+
+        const int pairs = min(S::PAIRS, (NP - n0) >> 1);
+#pragma unroll 1
+        for (int p = 0; p < pairs; ++p) {
+          const int n = n0 + 2 * p;
+          const uint32_t* bp = tiles + p * S::PAIR_TILE + lane * S::PAIR_SPAN;
+          const float2 Ax = *reinterpret_cast<const float2*>(A2s + ch * NP + n);        // first channel
+          const float2 Ay = *reinterpret_cast<const float2*>(A2s + (ch + 1) * NP + n);  // second
+          const f32x2 A0 = pack2(Ax.x, Ay.x), A1 = pack2(Ax.y, Ay.y);
+          f32x2 a0[kScanK], a1[kScanK];
+          f32x2 h0 = 0ull, h1 = 0ull;
+          {
+            const PairSpan<T_> B(bp);
+#pragma unroll
+            for (int k = 0; k < kScanK; ++k) {
+              float x, z;
+              unpack2(mul2(s2[k], A0), x, z);
+              a0[k] = pack2(exp2_approx(x), exp2_approx(z));
+              unpack2(mul2(s2[k], A1), x, z);
+              a1[k] = pack2(exp2_approx(x), exp2_approx(z));
+              h0 = fma2(a0[k], h0, pack2(su[k].x * B.lo(k), su[k].y * B.lo(k)));
+              h1 = fma2(a1[k], h1, pack2(su[k].x * B.hi(k), su[k].y * B.hi(k)));
+            }
+          }
+          // join the warp's spans
+          __syncwarp();  // the starts of the pair before have been read
+          *reinterpret_cast<ulonglong2*>(my_end) = make_ulonglong2(h0, h1);
+          __syncwarp();
+          {
+            const float A2 = join_A2[n], h_in = join_state[n];
+            float e[4], d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[i] = join_ends[i * 4];
+              d[i] = exp2_approx(join_sum[i] * A2);
+            }
+            // this lane's four spans as one: E + D h
+            float E = fmaf(d[1], e[0], e[1]);
+            E = fmaf(d[2], E, e[2]);
+            E = fmaf(d[3], E, e[3]);
+            float D = (d[0] * d[1]) * (d[2] * d[3]);
+            // and the lanes before it
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              const float Eo = __shfl_up_sync(0xffffffffu, E, o), Do = __shfl_up_sync(0xffffffffu, D, o);
+              if (lane >= o) {
+                E = fmaf(D, Eo, E);
+                D *= Do;
+              }
+            }
+            if (lane >= 28) const_cast<float*>(join_state)[n] = fmaf(D, h_in, E);
+            if (!STATE_ONLY) {
+              const float Eo = __shfl_up_sync(0xffffffffu, E, 4), Do = __shfl_up_sync(0xffffffffu, D, 4);
+              float h = lane >= 4 ? fmaf(Do, h_in, Eo) : h_in;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                join_ends[i * 4] = h;
+                h = fmaf(d[i], h, e[i]);
+              }
+            }
+          }
+          if (STATE_ONLY) continue;
+          __syncwarp();
+          const ulonglong2 start = *reinterpret_cast<const ulonglong2*>(my_end);
+          h0 = start.x;
+          h1 = start.y;
+          const PairSpan<T_> B(bp), C(bp + S::PAIRS * S::PAIR_TILE);
 #pragma unroll
           for (int k = 0; k < kScanK; ++k) {
-            const ulonglong2 b4 = *reinterpret_cast<const ulonglong2*>(bp + k * kScanSlab);
-            const ulonglong2 c4 = *reinterpret_cast<const ulonglong2*>(cp + k * kScanSlab);
-            h01 = fma2(a01[k], h01, mul2(su2[k], b4.x));
-            h23 = fma2(a23[k], h23, mul2(su2[k], b4.y));
-            y2[k] = fma2(h01, c4.x, y2[k]);
-            y2[k] = fma2(h23, c4.y, y2[k]);
+            h0 = fma2(a0[k], h0, pack2(su[k].x * B.lo(k), su[k].y * B.lo(k)));
+            h1 = fma2(a1[k], h1, pack2(su[k].x * B.hi(k), su[k].y * B.hi(k)));
+            float x, z;
+            unpack2(h0, x, z);
+            y[k].x = fmaf(x, C.lo(k), y[k].x);
+            y[k].y = fmaf(z, C.lo(k), y[k].y);
+            unpack2(h1, x, z);
+            y[k].x = fmaf(x, C.hi(k), y[k].x);
+            y[k].y = fmaf(z, C.hi(k), y[k].y);
           }
         }
       }
 
-      if (!STATE_ONLY && mine) {
-        T_* yp = a.Y + (row0 + t0 + mine0) * a.ldy + c;
+      if (!STATE_ONLY) {
+        copy_wait<1>();   // Z is in (the next step's copies may still run)
+        __syncthreads();
+        T_* zy = const_cast<T_*>(my_rows) + 2 * S::ROW_TILE;  // Z's place becomes Y's
 #pragma unroll
-        for (int k = 0; k < kScanK; ++k, yp += a.ldy) {
-          if (mine0 + k < tokens) {
-            float lo, hi;
-            unpack2(y2[k], lo, hi);
-            float y = lo + hi;
-            if (a.Z) y *= silu_gate(to_f32(rows[2 * kRawTile + k * kScanCh]));
-            *yp = from_f32<T_>(y);
+        for (int k = 0; k < kScanK; ++k) {
+          if (a.Z) {
+            const float2 z = load_two(zy + k * kScanCh);
+            y[k].x *= silu_gate(z.x);
+            y[k].y *= silu_gate(z.y);
           }
+          store_two(zy + k * kScanCh, y[k].x, y[k].y);
         }
+        __syncthreads();
+        store_rows(a.Y + (row0 + t0) * a.ldy + c0, rows + 2 * S::ROW_TILE, a.ldy, tokens, nch, pieces_y);
       }
     }
 
     __syncthreads();  // the state of the run's last token is complete
     if (STATE_ONLY) {
-      float* sums = reinterpret_cast<float*>(ends);
-      sums[tid] = steps_total;
-      __syncthreads();
       const long long at = ((long long)run * a.B + b) * a.d + c0;
-      if (tid < nch) {
-        float s = 0.f;
-        for (int i = 0; i < kScanSegs; ++i) s += sums[i * kScanCh + tid];
-        pl.step_sum[at + tid] = s;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        steps_total.x += __shfl_xor_sync(0xffffffffu, steps_total.x, o);
+        steps_total.y += __shfl_xor_sync(0xffffffffu, steps_total.y, o);
+      }
+      if (lane == 0) {
+        if (ch < nch) pl.step_sum[at + ch] = steps_total.x;
+        if (ch + 1 < nch) pl.step_sum[at + ch + 1] = steps_total.y;
       }
       for (int e = tid; e < nch * a.N; e += kScanThreads)
-        pl.carry[at * a.N + e] = state[(e / a.N) * (NP + 4) + e % a.N];
+        pl.carry[at * a.N + e] = state[(e / a.N) * NP + e % a.N];
       continue;
     }
     if (last) {
       if (a.state_out)
         for (int e = tid; e < nch * a.N; e += kScanThreads)
-          a.state_out[((long long)b * a.d + c0) * a.N + e] = state[(e / a.N) * (NP + 4) + e % a.N];
+          a.state_out[((long long)b * a.d + c0) * a.N + e] = state[(e / a.N) * NP + e % a.N];
     } else if (pl.chained) {
       for (int e = tid; e < kScanCh * NP; e += kScanThreads)
-        pl.carry[(long long)gb * kScanCh * NP + e] = state[(e / NP) * (NP + 4) + e % NP];
+        pl.carry[(long long)gb * kScanCh * NP + e] = state[e];
       __threadfence();
       __syncthreads();
       if (tid == 0) red_release_gpu_add(pl.flags + 1 + gb, 1u);
