@@ -493,8 +493,9 @@ ittt_status ittt_selective_scan_workspace_size(const ittt_scan_problem* p, size_
  * float32 (NULL: not wanted) h after each sequence's last one, and may be
  * state_in itself.  lengths as for ittt_causal_conv (a sequence of length 0
  * passes its state through).  Y must not overlap an input.  Everything is
- * computed and held in fp32; Y is rounded once.  Values that the formulas take
- * out of range come out inf or NaN as they would there. */
+ * computed and held in fp32; Y is rounded once.  Made for decay, s A <= 0: where
+ * s A > 0, the growth over any 256 tokens has to stay within fp32's range, and
+ * what leaves that range comes out inf or NaN. */
 ittt_status ittt_selective_scan(const ittt_scan_problem* p, const void* U, const void* delta,
                                 const float* A, const void* Bm, const void* Cm, const float* D,
                                 const float* dt_bias, const void* Z, const float* state_in,

@@ -300,7 +300,7 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   if (c.short_call) return c;
   c.per_group = int(cdiv(p->d / p->G, kScanCh));
   c.blocks = c.per_group * p->G;
-  const long long groups = p->B * c.blocks, workers = 2ll * sms;
+  const long long groups = p->B * c.blocks, workers = (long long)kScanCtas * sms;
   const long long chunks = cdiv(p->T, kScanChunk);
   long long run_chunks = chunks;
   if (groups * 4 >= workers * 3) {
@@ -351,7 +351,7 @@ ittt_status scan_chunks(const ScanArgs<T_>& a, const ScanPlan& pl, long long tas
   static std::atomic<bool> granted[kMaxDevices] = {};
   auto kern = scan_chunk_kernel<T_, STATE_ONLY>;
   if (!grant_smem(kern, scan_smem_bytes<T_>(256), granted)) return ITTT_ERR_CUDA;
-  return launch_clusters(kern, unsigned(std::min<long long>(tasks, 2ll * sms)), 1, kScanThreads,
+  return launch_clusters(kern, unsigned(std::min<long long>(tasks, (long long)kScanCtas * sms)), 1, kScanThreads,
                          scan_smem_bytes<T_>(a.N), st, a, pl, g_wait_ns.load());
 }
 

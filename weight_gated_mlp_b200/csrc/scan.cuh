@@ -7,13 +7,13 @@
 //
 //   scan_serial_kernel  short calls and single tokens: lanes over the state, four
 //       or eight elements a lane, token after token.  Bound by the state's bytes.
-//   scan_chunk_kernel   prompts: 16 channels a CTA, 256 tokens at a time.  A
+//   scan_chunk_kernel   prompts: 8 channels a CTA, 256 tokens at a time.  A
 //       thread owns two neighbouring channels and 8 consecutive tokens, a warp two
-//       channels and the whole chunk.  For two state elements at once a thread runs
-//       the recurrence from zero over its tokens and keeps the exponentials; the
-//       warp joins its 32 spans (a span's decay is exp(A sum s): one exponential
-//       and one rounding for 8 tokens); the thread runs its tokens again from the
-//       true state, with the kept exponentials, into y.  Two channels a thread halve
+//       channels and the whole chunk.  For four state elements at once a thread runs
+//       the recurrence of its tokens from zero into y, and keeps for each token
+//       g = C times the decay since the span's start; the warp joins its 32 spans (a
+//       span's decay is exp(A sum s): one exponential and one rounding for 8
+//       tokens); then y += g h with the span's true start h.  Two channels a thread halve
 //       what a state element costs in shared-memory reads of B and C (32 words a
 //       clock and SM, however many lanes read the same word), and the joins stay
 //       inside a warp, so the CTA meets four times a chunk only.
@@ -178,10 +178,17 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, 
 
 // ---------------------------------------------------------------- prompts
 
-constexpr int kScanThreads = 256;
-constexpr int kScanCh = 16;                       // channels a CTA, two a warp
+// Four warps and 168 registers a thread, three CTAs an SM, two pairs at once:
+// 470 us for 8192 x 5120 x 16 in bf16; one pair at once 491 us, with 128 registers
+// and four CTAs 534 us (584 us with two pairs, which then spill), eight warps and
+// 128 registers 514 us, 255 registers and two CTAs 532 us.
+constexpr int kScanWarps = 4;
+constexpr int kScanThreads = 32 * kScanWarps;
+constexpr int kScanCtas = 3;              // CTAs an SM
+constexpr int kScanCh = 2 * kScanWarps;           // channels a CTA, two a warp
 constexpr int kScanK = 8;                         // tokens a span, one span a lane
 constexpr int kScanChunk = 32 * kScanK;           // tokens a chunk
+constexpr int kScanJ = 2;                    // pairs of state elements at once
 
 // How the work of a call is cut.  A task is one channel block of one sequence
 // over one run of tokens; tasks are handed out run by run.
@@ -192,7 +199,7 @@ struct ScanPlan {
   int run_tokens;  // a multiple of kScanChunk
   int chained;     // 1: a run starts from the state that the run before leaves in
                    // `carry`; 0: run r from carry[r - 1] (filled by scan_join_kernel)
-  float* carry;    // chained: [B blocks][16 NP]; else [runs - 1][B, d, N]
+  float* carry;    // chained: [B blocks][kScanCh NP]; else [runs - 1][B, d, N]
   float* step_sum; // state pass: [runs - 1][B, d], the runs' sums of s
   unsigned* flags; // chained: [0] the next task, [1 + B blocks] runs finished
 };
@@ -215,12 +222,17 @@ struct ScanShape {
   static constexpr int RAW = 2 * kScanChunk * 32;            // bytes: B and C as they come
   static constexpr int TILES = 2 * PAIRS * PAIR_TILE * 4;    // bytes: B and C laid out
 };
-constexpr int kEndsWarp = 32 * 4 + 8 * 4;  // a warp's end states: 4 floats a span, 4 more every 4 spans
-__host__ __device__ constexpr int scan_np(int N) { return (N + 1) & ~1; }
+// A join: a lane takes one of the 4 J state elements (of two channels) that are
+// computed at once, over kJoinSpans neighbouring spans; 32 / (4 J) lanes share one.
+constexpr int kJoinSpans = 4 * kScanJ;
+constexpr int kEndsSpan = 4 * kScanJ;                       // floats of a span's end states
+constexpr int kEndsGroup = kJoinSpans * kEndsSpan + kEndsSpan;  // the groups on different banks
+constexpr int kEndsWarp = 32 / kJoinSpans * kEndsGroup;
+__host__ __device__ constexpr int scan_np(int N) { return (N + 2 * kScanJ - 1) / (2 * kScanJ) * (2 * kScanJ); }
 template <typename T_>
 __host__ __device__ constexpr int scan_smem_bytes(int N) {
   using S = ScanShape<T_>;
-  return S::ROWS + S::RAW + S::TILES + 8 * kEndsWarp * 4 + 2 * kScanCh * scan_np(N) * 4;
+  return S::ROWS + S::RAW + S::TILES + kScanWarps * kEndsWarp * 4 + 2 * kScanCh * scan_np(N) * 4;
 }
 
 // 16 bytes global -> shared, not waited for; zeros where valid is false.
@@ -314,22 +326,24 @@ __device__ __forceinline__ void fetch_slab(T_* dst, const T_* src, long long ld,
   }
 }
 
-// [token][SLAB] -> [pair][span][token]: one token a thread.
+// [token][SLAB] -> [pair][span][token].
 template <typename T_>
 __device__ __forceinline__ void lay_out(uint32_t* tile, const T_* raw) {
   using S = ScanShape<T_>;
-  const int t = threadIdx.x;
-  const uint4* src = reinterpret_cast<const uint4*>(raw + t * S::SLAB);
-  const uint4 lo = src[0], hi = src[1];
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  uint32_t* dst = tile + (t / kScanK) * S::PAIR_SPAN + (t % kScanK) * (S::ES / 2);
-  if (S::ES == 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dst[i * S::PAIR_TILE] = w[i];
-  } else {
+  for (int t = threadIdx.x; t < kScanChunk; t += kScanThreads) {
+    const uint4* src = reinterpret_cast<const uint4*>(raw + t * S::SLAB);
+    const uint4 lo = src[0], hi = src[1];
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t* dst = tile + (t / kScanK) * S::PAIR_SPAN + (t % kScanK) * (S::ES / 2);
+    if (S::ES == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint2*>(dst + i * S::PAIR_TILE) = make_uint2(w[2 * i], w[2 * i + 1]);
+      for (int i = 0; i < 8; ++i) dst[i * S::PAIR_TILE] = w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint2*>(dst + i * S::PAIR_TILE) = make_uint2(w[2 * i], w[2 * i + 1]);
+    }
   }
 }
 
@@ -376,7 +390,7 @@ __device__ __forceinline__ void store_two(float* p, float x, float y) {
 // STATE_ONLY: the first of the two passes of a call that is split over time: every
 // run from a zero state, its end state and sum of steps written, no outputs.
 template <typename T_, bool STATE_ONLY>
-__global__ void __launch_bounds__(kScanThreads, 2)
+__global__ void __launch_bounds__(kScanThreads, kScanCtas)
     scan_chunk_kernel(const ScanArgs<T_> a, const ScanPlan pl, unsigned long long wait_ns) {
   using S = ScanShape<T_>;
   extern __shared__ __align__(16) uint8_t scan_smem[];
@@ -385,7 +399,7 @@ __global__ void __launch_bounds__(kScanThreads, 2)
   T_* raw = reinterpret_cast<T_*>(scan_smem + S::ROWS);               // B, C as they come
   uint32_t* tiles = reinterpret_cast<uint32_t*>(scan_smem + S::ROWS + S::RAW);
   float* ends_all = reinterpret_cast<float*>(scan_smem + S::ROWS + S::RAW + S::TILES);
-  float* state = ends_all + 8 * kEndsWarp;                            // [ch][NP]
+  float* state = ends_all + kScanWarps * kEndsWarp;                            // [ch][NP]
   float* A2s = state + kScanCh * NP;                                  // [ch][NP], A log2(e)
   __shared__ int next_task, aborted;
 
@@ -396,12 +410,12 @@ __global__ void __launch_bounds__(kScanThreads, 2)
   const bool pieces_u = pieces_ok(a.U, a.ldu, dg), pieces_t = pieces_ok(a.delta, a.ldt, dg);
   const bool pieces_z = pieces_ok(a.Z, a.ldz, dg), pieces_y = pieces_ok(a.Y, a.ldy, dg);
   const bool pieces_b = pieces_ok(a.Bm, a.ldb, a.N), pieces_c = pieces_ok(a.Cm, a.ldc, a.N);
-  // joins: lane -> one state element of one channel (q = 2 element + channel) and 4 spans
+  // joins: lane -> one state element of one channel (q = 2 element + channel)
   float* ends = ends_all + warp * kEndsWarp;
-  float* my_end = ends + lane * 4 + (lane >> 2) * 4;
-  const int q = lane & 3, first_span = (lane >> 2) * 4;
-  float* join_ends = ends + first_span * 4 + (first_span >> 2) * 4 + q;
-  const float* join_state = state + (2 * warp + (q & 1)) * NP + (q >> 1);
+  float* my_end = ends + (lane / kJoinSpans) * kEndsGroup + (lane % kJoinSpans) * kEndsSpan;
+  const int q = lane % kEndsSpan, first_span = lane / kEndsSpan * kJoinSpans;
+  float* join_ends = ends + (lane / kEndsSpan) * kEndsGroup + q;
+  float* join_state = state + (2 * warp + (q & 1)) * NP + (q >> 1);
   const float* join_A2 = A2s + (2 * warp + (q & 1)) * NP + (q >> 1);
   if (tid == 0) aborted = 0;
   grid_dependency_wait();
@@ -504,8 +518,9 @@ __global__ void __launch_bounds__(kScanThreads, 2)
       const int tokens = min(kScanChunk, t_end - t0);
       const int mine0 = lane * kScanK;  // this thread's first token of the chunk
       f32x2 s2[kScanK];                 // (channel, next channel)
-      float2 su[kScanK], y[kScanK];
-      float join_sum[4];                // sums of s of the four spans that this lane joins
+      f32x2 y2[kScanK];
+      float2 su[kScanK];
+      float join_sum[kJoinSpans];       // sums of s of the spans that this lane joins
 
       for (int n0 = 0; n0 < NP; n0 += S::SLAB) {
         copy_wait<0>();
@@ -532,10 +547,10 @@ __global__ void __launch_bounds__(kScanThreads, 2)
             s2[k] = pack2(s.x, s.y);
             su[k] = make_float2(s.x * u.x, s.y * u.y);
             // no 0 * inf where there is no skip
-            y[k] = a.D ? make_float2(skip.x * u.x, skip.y * u.y) : make_float2(0.f, 0.f);
+            y2[k] = a.D ? pack2(skip.x * u.x, skip.y * u.y) : pack2(0.f, 0.f);
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kJoinSpans; ++i) {
             const float x = __shfl_sync(0xffffffffu, sum.x, first_span + i);
             const float z = __shfl_sync(0xffffffffu, sum.y, first_span + i);
             join_sum[i] = (q & 1) ? z : x;
@@ -559,81 +574,97 @@ __global__ void __launch_bounds__(kScanThreads, 2)
 
         const int pairs = min(S::PAIRS, (NP - n0) >> 1);
 #pragma unroll 1
-        for (int p = 0; p < pairs; ++p) {
+        for (int p = 0; p < pairs; p += kScanJ) {
           const int n = n0 + 2 * p;
-          const uint32_t* bp = tiles + p * S::PAIR_TILE + lane * S::PAIR_SPAN;
-          const float2 Ax = *reinterpret_cast<const float2*>(A2s + ch * NP + n);        // first channel
-          const float2 Ay = *reinterpret_cast<const float2*>(A2s + (ch + 1) * NP + n);  // second
-          const f32x2 A0 = pack2(Ax.x, Ay.x), A1 = pack2(Ax.y, Ay.y);
-          f32x2 a0[kScanK], a1[kScanK];
-          f32x2 h0 = 0ull, h1 = 0ull;
-          {
-            const PairSpan<T_> B(bp);
+          // the recurrence from zero, its outputs, and g = C times the decay since the
+          // span's start, which the start state is multiplied with once it is known
+          f32x2 g[kScanJ][2][kScanK], h[kScanJ][2];
+#pragma unroll
+          for (int j = 0; j < kScanJ; ++j) {
+            const uint32_t* bp = tiles + (p + j) * S::PAIR_TILE + lane * S::PAIR_SPAN;
+            const float2 Ax = *reinterpret_cast<const float2*>(A2s + ch * NP + n + 2 * j);
+            const float2 Ay = *reinterpret_cast<const float2*>(A2s + (ch + 1) * NP + n + 2 * j);
+            const f32x2 A0 = pack2(Ax.x, Ay.x), A1 = pack2(Ax.y, Ay.y);
+            const PairSpan<T_> B(bp), C(bp + S::PAIRS * S::PAIR_TILE);
+            f32x2 h0 = 0ull, h1 = 0ull, p0 = 0ull, p1 = 0ull;
 #pragma unroll
             for (int k = 0; k < kScanK; ++k) {
               float x, z;
               unpack2(mul2(s2[k], A0), x, z);
-              a0[k] = pack2(exp2_approx(x), exp2_approx(z));
+              const f32x2 a0 = pack2(exp2_approx(x), exp2_approx(z));
               unpack2(mul2(s2[k], A1), x, z);
-              a1[k] = pack2(exp2_approx(x), exp2_approx(z));
-              h0 = fma2(a0[k], h0, pack2(su[k].x * B.lo(k), su[k].y * B.lo(k)));
-              h1 = fma2(a1[k], h1, pack2(su[k].x * B.hi(k), su[k].y * B.hi(k)));
+              const f32x2 a1 = pack2(exp2_approx(x), exp2_approx(z));
+              h0 = fma2(a0, h0, pack2(su[k].x * B.lo(k), su[k].y * B.lo(k)));
+              h1 = fma2(a1, h1, pack2(su[k].x * B.hi(k), su[k].y * B.hi(k)));
+              if (!STATE_ONLY) {
+                p0 = k ? mul2(p0, a0) : a0;
+                p1 = k ? mul2(p1, a1) : a1;
+                float y0, y1;
+                unpack2(y2[k], y0, y1);
+                unpack2(h0, x, z);
+                y0 = fmaf(x, C.lo(k), y0);
+                y1 = fmaf(z, C.lo(k), y1);
+                unpack2(h1, x, z);
+                y2[k] = pack2(fmaf(x, C.hi(k), y0), fmaf(z, C.hi(k), y1));
+                unpack2(p0, x, z);
+                g[j][0][k] = pack2(x * C.lo(k), z * C.lo(k));
+                unpack2(p1, x, z);
+                g[j][1][k] = pack2(x * C.hi(k), z * C.hi(k));
+              }
             }
+            h[j][0] = h0;
+            h[j][1] = h1;
           }
           // join the warp's spans
-          __syncwarp();  // the starts of the pair before have been read
-          *reinterpret_cast<ulonglong2*>(my_end) = make_ulonglong2(h0, h1);
+          __syncwarp();  // the starts of the pairs before have been read
+#pragma unroll
+          for (int j = 0; j < kScanJ; ++j)
+            *reinterpret_cast<ulonglong2*>(my_end + 4 * j) = make_ulonglong2(h[j][0], h[j][1]);
           __syncwarp();
           {
             const float A2 = join_A2[n], h_in = join_state[n];
-            float e[4], d[4];
+            float e[kJoinSpans], d[kJoinSpans];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e[i] = join_ends[i * 4];
+            for (int i = 0; i < kJoinSpans; ++i) {
+              e[i] = join_ends[i * kEndsSpan];
               d[i] = exp2_approx(join_sum[i] * A2);
             }
-            // this lane's four spans as one: E + D h
-            float E = fmaf(d[1], e[0], e[1]);
-            E = fmaf(d[2], E, e[2]);
-            E = fmaf(d[3], E, e[3]);
-            float D = (d[0] * d[1]) * (d[2] * d[3]);
+            // this lane's spans as one: E + D h
+            float E = e[0], D = d[0];
+#pragma unroll
+            for (int i = 1; i < kJoinSpans; ++i) {
+              E = fmaf(d[i], E, e[i]);
+              D *= d[i];
+            }
             // and the lanes before it
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
+            for (int o = kEndsSpan; o < 32; o <<= 1) {
               const float Eo = __shfl_up_sync(0xffffffffu, E, o), Do = __shfl_up_sync(0xffffffffu, D, o);
               if (lane >= o) {
                 E = fmaf(D, Eo, E);
                 D *= Do;
               }
             }
-            if (lane >= 28) const_cast<float*>(join_state)[n] = fmaf(D, h_in, E);
+            if (lane >= 32 - kEndsSpan) join_state[n] = fmaf(D, h_in, E);
             if (!STATE_ONLY) {
-              const float Eo = __shfl_up_sync(0xffffffffu, E, 4), Do = __shfl_up_sync(0xffffffffu, D, 4);
-              float h = lane >= 4 ? fmaf(Do, h_in, Eo) : h_in;
+              const float Eo = __shfl_up_sync(0xffffffffu, E, kEndsSpan);
+              const float Do = __shfl_up_sync(0xffffffffu, D, kEndsSpan);
+              float start = lane >= kEndsSpan ? fmaf(Do, h_in, Eo) : h_in;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                join_ends[i * 4] = h;
-                h = fmaf(d[i], h, e[i]);
+              for (int i = 0; i < kJoinSpans; ++i) {
+                join_ends[i * kEndsSpan] = start;
+                start = fmaf(d[i], start, e[i]);
               }
             }
           }
           if (STATE_ONLY) continue;
           __syncwarp();
-          const ulonglong2 start = *reinterpret_cast<const ulonglong2*>(my_end);
-          h0 = start.x;
-          h1 = start.y;
-          const PairSpan<T_> B(bp), C(bp + S::PAIRS * S::PAIR_TILE);
 #pragma unroll
-          for (int k = 0; k < kScanK; ++k) {
-            h0 = fma2(a0[k], h0, pack2(su[k].x * B.lo(k), su[k].y * B.lo(k)));
-            h1 = fma2(a1[k], h1, pack2(su[k].x * B.hi(k), su[k].y * B.hi(k)));
-            float x, z;
-            unpack2(h0, x, z);
-            y[k].x = fmaf(x, C.lo(k), y[k].x);
-            y[k].y = fmaf(z, C.lo(k), y[k].y);
-            unpack2(h1, x, z);
-            y[k].x = fmaf(x, C.hi(k), y[k].x);
-            y[k].y = fmaf(z, C.hi(k), y[k].y);
+          for (int j = 0; j < kScanJ; ++j) {
+            const ulonglong2 start = *reinterpret_cast<const ulonglong2*>(my_end + 4 * j);
+#pragma unroll
+            for (int k = 0; k < kScanK; ++k)
+              y2[k] = fma2(g[j][1][k], start.y, fma2(g[j][0][k], start.x, y2[k]));
           }
         }
       }
@@ -644,12 +675,14 @@ __global__ void __launch_bounds__(kScanThreads, 2)
         T_* zy = const_cast<T_*>(my_rows) + 2 * S::ROW_TILE;  // Z's place becomes Y's
 #pragma unroll
         for (int k = 0; k < kScanK; ++k) {
+          float y0, y1;
+          unpack2(y2[k], y0, y1);
           if (a.Z) {
             const float2 z = load_two(zy + k * kScanCh);
-            y[k].x *= silu_gate(z.x);
-            y[k].y *= silu_gate(z.y);
+            y0 *= silu_gate(z.x);
+            y1 *= silu_gate(z.y);
           }
-          store_two(zy + k * kScanCh, y[k].x, y[k].y);
+          store_two(zy + k * kScanCh, y0, y1);
         }
         __syncthreads();
         store_rows(a.Y + (row0 + t0) * a.ldy + c0, rows + 2 * S::ROW_TILE, a.ldy, tokens, nch, pieces_y);
