@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "linear_f32.cuh"
 #include "mixer.cuh"
 #include "scan.cuh"
 #include "simt.cuh"

@@ -21,12 +21,25 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// act(x) in fp32.  SiLU at -inf: e^inf = inf, x / inf would be NaN in a quotient
-// of infinities; the limit, 0, is taken there.
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// x / (1 + e^-x) by the hardware's quotient (2 ulp).  Below -126 the value is
+// under 2^-174: 0 there, also at -inf, where the quotient would be NaN.
+__device__ __forceinline__ float silu_fast(float x) {
+  return x < -126.f ? 0.f : __fdividef(x, 1.f + exp2_approx(-kLog2e * x));
+}
+
+// act(x) in fp32; at -inf the limit (0 for all but the identity).
 __device__ __forceinline__ float activate(float x, int act) {
   switch (act) {
     case ITTT_ACT_RELU: return x < 0.f ? 0.f : x;  // NaN stays NaN
-    case ITTT_ACT_SILU: return x == -INFINITY ? 0.f : x / (1.f + expf(-x));
+    case ITTT_ACT_SILU: return silu_fast(x);
     case ITTT_ACT_GELU: return x == -INFINITY ? 0.f : 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
     case ITTT_ACT_GELU_TANH: {
       if (x == -INFINITY) return 0.f;
@@ -47,50 +60,6 @@ struct LinearArgs {
   int M, N, K, act;
 };
 
-// One 64 x 64 tile of Y per CTA on the CUDA cores, 4 x 4 outputs a thread.
-template <typename T_>
-__global__ void __launch_bounds__(256) linear_simt_kernel(const LinearArgs<T_> a) {
-  __shared__ float xs[16][64 + 4], ws[16][64 + 4];
-  grid_dependency_wait();
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 16) {
-    for (int e = threadIdx.x; e < 16 * 64; e += 256) {
-      const int kk = e % 16, r = e / 16;
-      const int m = m0 + r, n = n0 + r, k = k0 + kk;
-      xs[kk][r] = (m < a.M && k < a.K) ? to_f32(a.X[m * a.ldx + k]) : 0.f;
-      ws[kk][r] = (n < a.N && k < a.K) ? to_f32(a.W[(long long)n * a.K + k]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk) {
-      float x[4], w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = xs[kk][ty * 4 + i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = ws[kk][tx * 4 + j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m >= a.M || n >= a.N) continue;
-      float v = acc[i][j];
-      if (a.bias) v += to_f32(a.bias[n]);
-      v = activate(v, a.act);
-      if (a.residual) v += to_f32(a.residual[m * a.ldr + n]);
-      a.Y[m * a.ldy + n] = from_f32<T_>(v);
-    }
-}
-
 // ------------------------------------------------------------- causal conv
 
 template <typename T_>
@@ -106,10 +75,92 @@ __device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, in
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-// One output per thread.  The threads of token 0 also move the state: each reads
-// its channel's state_in before it writes the same channel's state_out, so the
-// two may be one buffer (the outputs of the first k - 1 tokens need state_in
-// too and are computed by the same thread).
+// Bound by reading X and writing Y once.  A thread owns the channels of 16 bytes
+// (8 bf16, 4 fp32) over RUN tokens: its RUN + KT - 1 rows are loaded before any
+// arithmetic, so that a warp keeps as many 512-byte requests in flight, and a run
+// re-reads KT - 1 rows of the run before (from L2).
+// The threads of token 0 also move the state: each reads its channels' state_in
+// (nobody else does: RUN >= KT - 1 for the runs behind) before it writes the same
+// channels' state_out, so the two may be one buffer.
+template <typename T_, int KT, int RUN>
+__global__ void __launch_bounds__(128) causal_conv_vec_kernel(const CausalConvArgs<T_> a,
+                                                              unsigned total, unsigned groups,
+                                                              unsigned runs) {
+  constexpr int V = 16 / int(sizeof(T_));
+  static_assert(RUN == 1 || RUN >= KT - 1, "only the first run reads state_in");
+  grid_dependency_wait();
+  const unsigned e = blockIdx.x * 128u + threadIdx.x;
+  if (e >= total) return;
+  const unsigned rest = e / groups;
+  const int c = static_cast<int>(e - rest * groups) * V;
+  const int b = static_cast<int>(rest / runs);
+  const int t0 = static_cast<int>(rest - unsigned(b) * runs) * RUN;
+  const int len = sequence_length(a.lengths, b, a.T);
+  const T_* X = a.X + (long long)b * a.T * a.ldx + c;
+  const T_* s_in = a.state_in ? a.state_in + (long long)b * (KT - 1) * a.d + c : nullptr;
+  auto row = [&](int t) -> uint4 {  // the inputs of token t >= -(KT - 1)
+    if (t >= 0) return *reinterpret_cast<const uint4*>(X + t * a.ldx);
+    if (s_in) return *reinterpret_cast<const uint4*>(s_in + (long long)(t + KT - 1) * a.d);
+    return make_uint4(0u, 0u, 0u, 0u);
+  };
+  if (t0 < len) {
+    uint4 rows[RUN + KT - 1];
+#pragma unroll
+    for (int i = 0; i < RUN + KT - 1; ++i)
+      rows[i] = t0 + i - (KT - 1) < len ? row(t0 + i - (KT - 1)) : make_uint4(0u, 0u, 0u, 0u);
+    float w[KT][V], bias[V];
+    {
+      // the taps of V channels are V * KT contiguous elements
+      const uint4* wp = reinterpret_cast<const uint4*>(a.w + (long long)c * KT);
+      T_ taps[V * KT];
+#pragma unroll
+      for (int i = 0; i < KT; ++i) *reinterpret_cast<uint4*>(taps + i * V) = __ldg(wp + i);
+#pragma unroll
+      for (int j = 0; j < KT; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[j][i] = to_f32(taps[i * KT + j]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) bias[i] = a.bias ? to_f32(a.bias[c + i]) : 0.f;
+    }
+    T_* Y = a.Y + ((long long)b * a.T + t0) * a.ldy + c;
+#pragma unroll
+    for (int t = 0; t < RUN; ++t) {
+      if (t0 + t < len) {
+        float y[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = bias[i];
+#pragma unroll
+        for (int j = 0; j < KT; ++j) {
+          const T_* x = reinterpret_cast<const T_*>(&rows[t + j]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) y[i] = fmaf(w[j][i], to_f32(x[i]), y[i]);
+        }
+        uint4 out;
+        T_* o = reinterpret_cast<T_*>(&out);
+        if (a.act == ITTT_ACT_SILU) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = from_f32<T_>(silu_fast(y[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = from_f32<T_>(activate(y[i], a.act));
+        }
+        *reinterpret_cast<uint4*>(Y + t * a.ldy) = out;
+      }
+    }
+  }
+  if (KT > 1 && t0 == 0 && a.state_out) {
+    uint4 keep[KT > 1 ? KT - 1 : 1];
+#pragma unroll
+    for (int j = 0; j < KT - 1; ++j) keep[j] = row(len - (KT - 1) + j);
+    T_* s_out = a.state_out + (long long)b * (KT - 1) * a.d + c;
+#pragma unroll
+    for (int j = 0; j < KT - 1; ++j) *reinterpret_cast<uint4*>(s_out + (long long)j * a.d) = keep[j];
+  }
+}
+
+// Any width, alignment and number of taps: one channel a thread, 16 tokens (or, in
+// CTA row 0, the first k - 1 tokens and the state, with the same order of reads
+// and writes).
 template <typename T_>
 __global__ void __launch_bounds__(256) causal_conv_kernel(const CausalConvArgs<T_> a) {
   grid_dependency_wait();

@@ -57,13 +57,6 @@ LinearArgs<T_> linear_args(const ittt_linear_problem* p, const void* X, const vo
   return a;
 }
 
-ittt_status linear_f32(const LinearArgs<float>& a, cudaStream_t st) {
-  const long long gy = cdiv(a.M, 64);
-  if (gy > 65535) return ITTT_ERR_UNSUPPORTED;
-  return launch_pdl(linear_simt_kernel<float>, dim3(unsigned(cdiv(a.N, 64)), unsigned(gy)), dim3(256),
-                    st, a);
-}
-
 // A launch in clusters of `cluster` CTAs, its prologue overlapping the kernel before.
 template <typename... KArgs, typename... Args>
 ittt_status launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned cluster, unsigned threads,
@@ -85,6 +78,43 @@ ittt_status launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned clus
   if (cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...) != cudaSuccess)
     return ITTT_ERR_CUDA;
   return launch_status();
+}
+
+template <int MB, bool VEC>
+ittt_status linear_gemv(const LinearArgs<float>& a, cudaStream_t st) {
+  return launch_pdl(linear_gemv_kernel<MB, VEC>, dim3(unsigned(cdiv(a.N, 4))), dim3(128), st, a);
+}
+
+template <int BM, int BN, int TM, int TN, bool VEC>
+ittt_status linear_tiles_f32(const LinearArgs<float>& a, int splits, cudaStream_t st) {
+  const long long m_tiles = cdiv(a.M, BM), grid = m_tiles * cdiv(a.N, BN) * splits;
+  if (grid >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
+  return launch_clusters(linear_f32_kernel<BM, BN, TM, TN, VEC>, unsigned(grid), unsigned(splits),
+                         F32Tile<BM, BN, TM, TN>::THREADS, 0, st, a, int(m_tiles));
+}
+
+// Up to 8 rows: the kernel that streams W.  128 x 128 tiles when they fill the
+// SMs; else 64 x 64 tiles, K split over clusters while the CTAs stay within four
+// an SM and every CTA keeps at least 64 columns of K.
+template <bool VEC>
+ittt_status linear_f32_sized(const LinearArgs<float>& a, int sms, cudaStream_t st) {
+  if (a.M == 1) return linear_gemv<1, VEC>(a, st);
+  if (a.M == 2) return linear_gemv<2, VEC>(a, st);
+  if (a.M <= 4) return linear_gemv<4, VEC>(a, st);
+  if (a.M <= 8) return linear_gemv<8, VEC>(a, st);
+  if (cdiv(a.M, 128) * cdiv(a.N, 128) >= sms) return linear_tiles_f32<128, 128, 8, 8, VEC>(a, 1, st);
+  const long long tiles = cdiv(a.M, 64) * cdiv(a.N, 64);
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= 4ll * sms && a.K >= 64 * splits * 2) splits *= 2;
+  return linear_tiles_f32<64, 64, 8, 4, VEC>(a, splits, st);
+}
+
+ittt_status linear_f32(const LinearArgs<float>& a, cudaStream_t st) {
+  const int sms = num_sms();
+  if (sms <= 0) return ITTT_ERR_CUDA;
+  if (aligned16(a.X) && aligned16(a.W) && a.K % 4 == 0 && a.ldx % 4 == 0)
+    return linear_f32_sized<true>(a, sms, st);
+  return linear_f32_sized<false>(a, sms, st);
 }
 
 // Dynamic shared memory above the default, granted once per kernel and device.
@@ -208,6 +238,20 @@ ittt_status validate_conv(const ittt_conv_problem* p) {
   return ITTT_OK;
 }
 
+// Single tokens: one token a thread; else runs of eight.
+template <typename T_, int KT>
+ittt_status causal_conv_vec(const CausalConvArgs<T_>& a, cudaStream_t st) {
+  const long long groups = a.d / (16 / int(sizeof(T_))), run = a.T == 1 ? 1 : 8;
+  const long long runs = cdiv(a.T, run), total = a.B * runs * groups;
+  if (total >= (1ll << 32) - 128) return ITTT_ERR_UNSUPPORTED;
+  const dim3 grid(unsigned(cdiv(total, 128)));
+  if (a.T == 1)
+    return launch_pdl(causal_conv_vec_kernel<T_, KT, 1>, grid, dim3(128), st, a, unsigned(total),
+                      unsigned(groups), unsigned(runs));
+  return launch_pdl(causal_conv_vec_kernel<T_, KT, 8>, grid, dim3(128), st, a, unsigned(total),
+                    unsigned(groups), unsigned(runs));
+}
+
 template <typename T_>
 ittt_status causal_conv_launch(const ittt_conv_problem* p, const void* X, const void* w,
                                const void* bias, const void* state_in, const int32_t* lengths,
@@ -227,6 +271,21 @@ ittt_status causal_conv_launch(const ittt_conv_problem* p, const void* X, const 
   a.d = int(p->d);
   a.k = p->k;
   a.act = p->act;
+  constexpr int V = 16 / int(sizeof(T_));
+  const bool vec = p->k <= 8 && p->d % V == 0 && a.ldx % V == 0 && a.ldy % V == 0 && aligned16(X) &&
+                   aligned16(w) && aligned16(Y) && aligned16(a.state_in) && aligned16(a.state_out);
+  if (vec) {
+    switch (p->k) {
+      case 1: return causal_conv_vec<T_, 1>(a, st);
+      case 2: return causal_conv_vec<T_, 2>(a, st);
+      case 3: return causal_conv_vec<T_, 3>(a, st);
+      case 4: return causal_conv_vec<T_, 4>(a, st);
+      case 5: return causal_conv_vec<T_, 5>(a, st);
+      case 6: return causal_conv_vec<T_, 6>(a, st);
+      case 7: return causal_conv_vec<T_, 7>(a, st);
+      default: return causal_conv_vec<T_, 8>(a, st);
+    }
+  }
   const long long rest = p->T - (p->k - 1);
   const long long gy = 1 + (rest > 0 ? cdiv(rest, 16) : 0);
   if (gy > 65535) return ITTT_ERR_UNSUPPORTED;

@@ -24,8 +24,6 @@
 
 namespace ittt {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 template <typename T_>
 struct ScanArgs {
   const T_ *U, *delta, *Bm, *Cm, *Z;
@@ -36,12 +34,6 @@ struct ScanArgs {
   long long ldu, ldt, ldb, ldc, ldz, ldy;
   int B, T, d, N, G, softplus;
 };
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // softplus(x) = max(x, 0) + log(1 + e^-|x|).  log(1 + e) = e q(e) on [0, 1], q of
 // degree 9 fitted to least relative error (2^-23 in fp32 Horner steps): small
@@ -60,11 +52,6 @@ __device__ __forceinline__ float softplus_f32(float x) {
   q = fmaf(q, e, 1.0f);
   // NaN stays NaN (fmaxf alone would drop it)
   return fmaf(q, e, x != x ? x : fmaxf(x, 0.f));
-}
-
-// z / (1 + e^-z) by the hardware's quotient (2 ulp; a denominator past 2^126 gives 0).
-__device__ __forceinline__ float silu_gate(float z) {
-  return __fdividef(z, 1.f + exp2_approx(-kLog2e * z));
 }
 
 // Two fp32 values in one 64-bit register and the paired instructions on them
@@ -159,7 +146,7 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, 
     if (t < len && sub == 0 && real) {
       const long long row = row0 + t;
       if (a.D) y = fmaf(skip, u, y);
-      if (a.Z) y *= silu_gate(to_f32(a.Z[row * a.ldz + c]));
+      if (a.Z) y *= silu_fast(to_f32(a.Z[row * a.ldz + c]));
       a.Y[row * a.ldy + c] = from_f32<T_>(y);
     }
   }
@@ -679,8 +666,8 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas)
           unpack2(y2[k], y0, y1);
           if (a.Z) {
             const float2 z = load_two(zy + k * kScanCh);
-            y0 *= silu_gate(z.x);
-            y1 *= silu_gate(z.y);
+            y0 *= silu_fast(z.x);
+            y1 *= silu_fast(z.y);
           }
           store_two(zy + k * kScanCh, y0, y1);
         }

@@ -18,6 +18,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "linear_f32.cuh"
 #include "mixer.cuh"
 
 namespace ittt {
@@ -52,18 +53,6 @@ __device__ __forceinline__ void linear_store32(const LinearArgs<__nv_bfloat16>& 
       }
     }
   }
-}
-
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_address) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_address));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
 }
 
 // Shared-memory pipeline depth: about 100 KB, so that two CTAs share an SM and
