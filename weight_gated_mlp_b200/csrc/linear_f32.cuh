@@ -26,15 +26,16 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
+template <int ACT>
 __device__ __forceinline__ void linear_finish(const LinearArgs<float>& a, int m, int n, float v) {
   if (a.bias) v += a.bias[n];
-  v = activate(v, a.act);
+  v = activate<ACT>(v);
   if (a.residual) v += a.residual[m * a.ldr + n];
   a.Y[m * a.ldy + n] = v;
 }
 
 // VEC: 16-byte pieces of the rows of X and W.
-template <int MB, bool VEC>
+template <int ACT, int MB, bool VEC>
 __global__ void __launch_bounds__(128) linear_gemv_kernel(const LinearArgs<float> a) {
   constexpr int NB = 4;
   grid_dependency_wait();
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(128) linear_gemv_kernel(const LinearArgs<float
   if (threadIdx.x < MB * NB) {
     const int i = threadIdx.x / NB, n = n0 + threadIdx.x % NB;
     if (i < a.M && n < a.N)
-      linear_finish(a, i, n, (part[0][threadIdx.x] + part[1][threadIdx.x]) +
+      linear_finish<ACT>(a, i, n, (part[0][threadIdx.x] + part[1][threadIdx.x]) +
                                  (part[2][threadIdx.x] + part[3][threadIdx.x]));
   }
 }
@@ -125,7 +126,7 @@ __device__ __forceinline__ float4 f32_quad(const float* p, long long ld, int r, 
   return v;
 }
 
-template <int BM, int BN, int TM, int TN, bool VEC>
+template <int ACT, int BM, int BN, int TM, int TN, bool VEC>
 __global__ void __launch_bounds__(F32Tile<BM, BN, TM, TN>::THREADS)
     linear_f32_kernel(const LinearArgs<float> a, int m_tiles) {
   using S = F32Tile<BM, BN, TM, TN>;
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(F32Tile<BM, BN, TM, TN>::THREADS)
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
         const int n = n0 + col_of(j);
-        if (n < a.N) linear_finish(a, m, n, acc[i][j]);
+        if (n < a.N) linear_finish<ACT>(a, m, n, acc[i][j]);
       }
     }
     return;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(F32Tile<BM, BN, TM, TN>::THREADS)
 #pragma unroll
       for (int s = 1; s < 8; ++s)
         if (s < splits) v += part[s];
-      linear_finish(a, m0 + r, n0 + c, v);
+      linear_finish<ACT>(a, m0 + r, n0 + c, v);
     }
     cluster_sync_all();  // no CTA leaves while a peer may still read its sums
   }

@@ -3,6 +3,8 @@
 // scan.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace ittt {
@@ -35,17 +37,30 @@ __device__ __forceinline__ float silu_fast(float x) {
   return x < -126.f ? 0.f : __fdividef(x, 1.f + exp2_approx(-kLog2e * x));
 }
 
-// act(x) in fp32; at -inf the limit (0 for all but the identity).
-__device__ __forceinline__ float activate(float x, int act) {
+// act(x) in fp32; at -inf the limit (0 for all but the identity).  A template
+// argument, so that a kernel holds the instructions of its own activation only: with
+// all of them behind a switch in an unrolled epilogue, a short launch spent more
+// time fetching instructions than computing.
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if (ACT == ITTT_ACT_RELU) return x < 0.f ? 0.f : x;  // NaN stays NaN
+  if (ACT == ITTT_ACT_SILU) return silu_fast(x);
+  if (ACT == ITTT_ACT_GELU)
+    return x == -INFINITY ? 0.f : 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+  if (ACT == ITTT_ACT_GELU_TANH) {
+    const float t = 0.79788456080286536f * (x + 0.044715f * x * x * x);
+    return x == -INFINITY ? 0.f : 0.5f * x * (1.f + tanhf(t));
+  }
+  return x;
+}
+
+// The same by a run-time act, out of line.
+__device__ __noinline__ float activate_any(float x, int act) {
   switch (act) {
-    case ITTT_ACT_RELU: return x < 0.f ? 0.f : x;  // NaN stays NaN
-    case ITTT_ACT_SILU: return silu_fast(x);
-    case ITTT_ACT_GELU: return x == -INFINITY ? 0.f : 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
-    case ITTT_ACT_GELU_TANH: {
-      if (x == -INFINITY) return 0.f;
-      const float a = 0.79788456080286536f * (x + 0.044715f * x * x * x);
-      return 0.5f * x * (1.f + tanhf(a));
-    }
+    case ITTT_ACT_RELU: return activate<ITTT_ACT_RELU>(x);
+    case ITTT_ACT_SILU: return activate<ITTT_ACT_SILU>(x);
+    case ITTT_ACT_GELU: return activate<ITTT_ACT_GELU>(x);
+    case ITTT_ACT_GELU_TANH: return activate<ITTT_ACT_GELU_TANH>(x);
     default: return x;
   }
 }
@@ -75,18 +90,18 @@ __device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, in
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-// Bound by reading X and writing Y once.  A thread owns the channels of 16 bytes
-// (8 bf16, 4 fp32) over RUN tokens: its RUN + KT - 1 rows are loaded before any
-// arithmetic, so that a warp keeps as many 512-byte requests in flight, and a run
+// Bound by reading X and writing Y once.  A thread owns V neighbouring channels
+// (16 bytes; 1 where widths or alignment do not allow that) over RUN tokens: its RUN + KT - 1 rows are loaded before any
+// arithmetic, so that a warp keeps as many requests in flight, and a run
 // re-reads KT - 1 rows of the run before (from L2).
 // The threads of token 0 also move the state: each reads its channels' state_in
 // (nobody else does: RUN >= KT - 1 for the runs behind) before it writes the same
 // channels' state_out, so the two may be one buffer.
-template <typename T_, int KT, int RUN>
+template <typename T_, int V, int KT, int RUN, int ACT>
 __global__ void __launch_bounds__(128) causal_conv_vec_kernel(const CausalConvArgs<T_> a,
                                                               unsigned total, unsigned groups,
                                                               unsigned runs) {
-  constexpr int V = 16 / int(sizeof(T_));
+  using Row = std::conditional_t<V == 1, T_, uint4>;
   static_assert(RUN == 1 || RUN >= KT - 1, "only the first run reads state_in");
   grid_dependency_wait();
   const unsigned e = blockIdx.x * 128u + threadIdx.x;
@@ -98,23 +113,23 @@ __global__ void __launch_bounds__(128) causal_conv_vec_kernel(const CausalConvAr
   const int len = sequence_length(a.lengths, b, a.T);
   const T_* X = a.X + (long long)b * a.T * a.ldx + c;
   const T_* s_in = a.state_in ? a.state_in + (long long)b * (KT - 1) * a.d + c : nullptr;
-  auto row = [&](int t) -> uint4 {  // the inputs of token t >= -(KT - 1)
-    if (t >= 0) return *reinterpret_cast<const uint4*>(X + t * a.ldx);
-    if (s_in) return *reinterpret_cast<const uint4*>(s_in + (long long)(t + KT - 1) * a.d);
-    return make_uint4(0u, 0u, 0u, 0u);
+  auto row = [&](int t) -> Row {  // the inputs of token t >= -(KT - 1)
+    if (t >= 0) return *reinterpret_cast<const Row*>(X + t * a.ldx);
+    if (s_in) return *reinterpret_cast<const Row*>(s_in + (long long)(t + KT - 1) * a.d);
+    return Row{};
   };
   if (t0 < len) {
-    uint4 rows[RUN + KT - 1];
+    Row rows[RUN + KT - 1];
 #pragma unroll
     for (int i = 0; i < RUN + KT - 1; ++i)
-      rows[i] = t0 + i - (KT - 1) < len ? row(t0 + i - (KT - 1)) : make_uint4(0u, 0u, 0u, 0u);
+      rows[i] = t0 + i - (KT - 1) < len ? row(t0 + i - (KT - 1)) : Row{};
     float w[KT][V], bias[V];
     {
       // the taps of V channels are V * KT contiguous elements
-      const uint4* wp = reinterpret_cast<const uint4*>(a.w + (long long)c * KT);
-      T_ taps[V * KT];
+      const Row* wp = reinterpret_cast<const Row*>(a.w + (long long)c * KT);
+      alignas(16) T_ taps[V * KT];
 #pragma unroll
-      for (int i = 0; i < KT; ++i) *reinterpret_cast<uint4*>(taps + i * V) = __ldg(wp + i);
+      for (int i = 0; i < KT; ++i) *reinterpret_cast<Row*>(taps + i * V) = __ldg(wp + i);
 #pragma unroll
       for (int j = 0; j < KT; ++j)
 #pragma unroll
@@ -135,30 +150,32 @@ __global__ void __launch_bounds__(128) causal_conv_vec_kernel(const CausalConvAr
 #pragma unroll
           for (int i = 0; i < V; ++i) y[i] = fmaf(w[j][i], to_f32(x[i]), y[i]);
         }
-        uint4 out;
+        Row out;
         T_* o = reinterpret_cast<T_*>(&out);
-        if (a.act == ITTT_ACT_SILU) {
+        if (ACT == ITTT_ACT_SILU) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = from_f32<T_>(silu_fast(y[i]));
-        } else {
+          for (int i = 0; i < V; ++i) y[i] = silu_fast(y[i]);
+        } else if (ACT != ITTT_ACT_NONE) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = from_f32<T_>(activate(y[i], a.act));
+          for (int i = 0; i < V; ++i) y[i] = activate_any(y[i], a.act);
         }
-        *reinterpret_cast<uint4*>(Y + t * a.ldy) = out;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = from_f32<T_>(y[i]);
+        *reinterpret_cast<Row*>(Y + t * a.ldy) = out;
       }
     }
   }
   if (KT > 1 && t0 == 0 && a.state_out) {
-    uint4 keep[KT > 1 ? KT - 1 : 1];
+    Row keep[KT > 1 ? KT - 1 : 1];
 #pragma unroll
     for (int j = 0; j < KT - 1; ++j) keep[j] = row(len - (KT - 1) + j);
     T_* s_out = a.state_out + (long long)b * (KT - 1) * a.d + c;
 #pragma unroll
-    for (int j = 0; j < KT - 1; ++j) *reinterpret_cast<uint4*>(s_out + (long long)j * a.d) = keep[j];
+    for (int j = 0; j < KT - 1; ++j) *reinterpret_cast<Row*>(s_out + (long long)j * a.d) = keep[j];
   }
 }
 
-// Any width, alignment and number of taps: one channel a thread, 16 tokens (or, in
+// More than eight taps: one channel a thread, 16 tokens (or, in
 // CTA row 0, the first k - 1 tokens and the state, with the same order of reads
 // and writes).
 template <typename T_>
@@ -185,7 +202,7 @@ __global__ void __launch_bounds__(256) causal_conv_kernel(const CausalConvArgs<T
       else if (s_in) x = to_f32(s_in[(long long)(s + back) * a.d]);
       acc = fmaf(to_f32(w[j]), x, acc);
     }
-    Y[t * a.ldy] = from_f32<T_>(activate(acc, a.act));
+    Y[t * a.ldy] = from_f32<T_>(activate_any(acc, a.act));
   }
   if (blockIdx.y == 0 && a.state_out) {
     T_* s_out = a.state_out + (long long)b * back * a.d + c;

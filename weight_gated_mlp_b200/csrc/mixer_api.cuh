@@ -80,41 +80,42 @@ ittt_status launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned clus
   return launch_status();
 }
 
-template <int MB, bool VEC>
+template <int ACT, int MB, bool VEC>
 ittt_status linear_gemv(const LinearArgs<float>& a, cudaStream_t st) {
-  return launch_pdl(linear_gemv_kernel<MB, VEC>, dim3(unsigned(cdiv(a.N, 4))), dim3(128), st, a);
+  return launch_pdl(linear_gemv_kernel<ACT, MB, VEC>, dim3(unsigned(cdiv(a.N, 4))), dim3(128), st, a);
 }
 
-template <int BM, int BN, int TM, int TN, bool VEC>
+template <int ACT, int BM, int BN, int TM, int TN, bool VEC>
 ittt_status linear_tiles_f32(const LinearArgs<float>& a, int splits, cudaStream_t st) {
   const long long m_tiles = cdiv(a.M, BM), grid = m_tiles * cdiv(a.N, BN) * splits;
   if (grid >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
-  return launch_clusters(linear_f32_kernel<BM, BN, TM, TN, VEC>, unsigned(grid), unsigned(splits),
+  return launch_clusters(linear_f32_kernel<ACT, BM, BN, TM, TN, VEC>, unsigned(grid), unsigned(splits),
                          F32Tile<BM, BN, TM, TN>::THREADS, 0, st, a, int(m_tiles));
 }
 
 // Up to 8 rows: the kernel that streams W.  128 x 128 tiles when they fill the
-// SMs; else 64 x 64 tiles, K split over clusters while the CTAs stay within four
+// SMs; else 64 x 64 tiles, K split over clusters while the CTAs stay within six
 // an SM and every CTA keeps at least 64 columns of K.
-template <bool VEC>
+template <int ACT, bool VEC>
 ittt_status linear_f32_sized(const LinearArgs<float>& a, int sms, cudaStream_t st) {
-  if (a.M == 1) return linear_gemv<1, VEC>(a, st);
-  if (a.M == 2) return linear_gemv<2, VEC>(a, st);
-  if (a.M <= 4) return linear_gemv<4, VEC>(a, st);
-  if (a.M <= 8) return linear_gemv<8, VEC>(a, st);
-  if (cdiv(a.M, 128) * cdiv(a.N, 128) >= sms) return linear_tiles_f32<128, 128, 8, 8, VEC>(a, 1, st);
+  if (a.M == 1) return linear_gemv<ACT, 1, VEC>(a, st);
+  if (a.M == 2) return linear_gemv<ACT, 2, VEC>(a, st);
+  if (a.M <= 4) return linear_gemv<ACT, 4, VEC>(a, st);
+  if (a.M <= 8) return linear_gemv<ACT, 8, VEC>(a, st);
+  if (cdiv(a.M, 128) * cdiv(a.N, 128) >= sms) return linear_tiles_f32<ACT, 128, 128, 8, 8, VEC>(a, 1, st);
   const long long tiles = cdiv(a.M, 64) * cdiv(a.N, 64);
   int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= 4ll * sms && a.K >= 64 * splits * 2) splits *= 2;
-  return linear_tiles_f32<64, 64, 8, 4, VEC>(a, splits, st);
+  while (splits < 8 && tiles * splits * 2 <= 6ll * sms && a.K >= 64 * splits * 2) splits *= 2;
+  return linear_tiles_f32<ACT, 64, 64, 8, 8, VEC>(a, splits, st);
 }
 
+template <int ACT>
 ittt_status linear_f32(const LinearArgs<float>& a, cudaStream_t st) {
   const int sms = num_sms();
   if (sms <= 0) return ITTT_ERR_CUDA;
   if (aligned16(a.X) && aligned16(a.W) && a.K % 4 == 0 && a.ldx % 4 == 0)
-    return linear_f32_sized<true>(a, sms, st);
-  return linear_f32_sized<false>(a, sms, st);
+    return linear_f32_sized<ACT, true>(a, sms, st);
+  return linear_f32_sized<ACT, false>(a, sms, st);
 }
 
 // Dynamic shared memory above the default, granted once per kernel and device.
@@ -130,18 +131,18 @@ bool grant_smem(Kern kern, int smem, std::atomic<bool>* done) {
 }
 
 // One 128 x MT tile per CTA, K split over clusters.  The split is the widest of
-// 1, 2, 4, 8 CTAs that leaves every CTA of the launch resident (two per SM) and
-// at least four k-blocks to each.
-template <int MT>
+// 1, 2, 4, 8 CTAs that leaves every CTA of the launch resident and at least four
+// k-blocks to each.
+template <int MT, int ACT>
 ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream_t st) {
   using S = SplitShape<MT>;
   static std::atomic<bool> granted[kMaxDevices] = {};
-  auto kern = linear_split_kernel<MT>;
+  auto kern = linear_split_kernel<MT, ACT>;
   if (!grant_smem(kern, S::SMEM, granted)) return ITTT_ERR_CUDA;
   const int num_kb = int(cdiv(a.K, 64));
   const long long m_tiles = cdiv(a.M, MT), tiles = m_tiles * cdiv(a.N, 128);
   int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= 2ll * sms && num_kb >= 4 * splits * 2) splits *= 2;
+  while (splits < 8 && tiles * splits * 2 <= (long long)S::CTAS * sms && num_kb >= 4 * splits * 2) splits *= 2;
   if (tiles * splits >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
   CUtensorMap w, x;
   if (!make_map(&w, a.W, a.K, a.N, a.K, 64, 128) || !make_map(&x, a.X, a.K, a.M, a.ldx, 64, MT))
@@ -151,10 +152,11 @@ ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream
 }
 
 // CTA pairs of linear_pair_kernel that the current device holds at once (0: none).
+template <int ACT>
 int resident_pairs(int sms) {
   static std::atomic<bool> granted[kMaxDevices] = {};
   static std::atomic<int> pairs[kMaxDevices] = {};
-  if (!grant_smem(linear_pair_kernel, kPairSmem, granted)) return 0;
+  if (!grant_smem(linear_pair_kernel<ACT>, kPairSmem, granted)) return 0;
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if ((n = pairs[dev].load(std::memory_order_relaxed)) > 0) return n;
@@ -169,12 +171,13 @@ int resident_pairs(int sms) {
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel, &cfg) != cudaSuccess || n <= 0) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, linear_pair_kernel<ACT>, &cfg) != cudaSuccess || n <= 0) return 0;
   pairs[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
 // Persistent CTA pairs.
+template <int ACT>
 ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int mt, int pairs, cudaStream_t st) {
   PairTile t{};
   t.mt = mt;
@@ -189,7 +192,7 @@ ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int mt, int pairs, 
   if (!make_map(&w, a.W, a.K, a.N, a.K, 64, 128) || !make_map(&x, a.X, a.K, a.M, a.ldx, 64, mt / 2))
     return ITTT_ERR_CUDA;
   const long long units = (long long)t.m_tiles * t.n_tiles;
-  return launch_clusters(linear_pair_kernel, unsigned(2 * std::min<long long>(units, pairs)), 2, 192,
+  return launch_clusters(linear_pair_kernel<ACT>, unsigned(2 * std::min<long long>(units, pairs)), 2, 192,
                          kPairSmem, st, w, x, a, t, g_wait_ns.load());
 }
 
@@ -198,14 +201,15 @@ ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int mt, int pairs, 
 // SMs, with the tile height (256, 224, ... 128 rows) whose waves of tiles cost
 // least; else 128 x 128 tiles, or 128 x 64 where even eight-fold splits of those
 // leave SMs empty.
+template <int ACT>
 ittt_status linear_bf16(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
   const int sms = num_sms();
   if (sms <= 0) return ITTT_ERR_CUDA;
-  if (a.M <= 16) return linear_split<16>(a, sms, st);
-  if (a.M <= 32) return linear_split<32>(a, sms, st);
-  if (a.M <= 64) return linear_split<64>(a, sms, st);
-  if (a.M <= 128) return linear_split<128>(a, sms, st);
-  const int pairs = resident_pairs(sms);
+  if (a.M <= 16) return linear_split<16, ACT>(a, sms, st);
+  if (a.M <= 32) return linear_split<32, ACT>(a, sms, st);
+  if (a.M <= 64) return linear_split<64, ACT>(a, sms, st);
+  if (a.M <= 128) return linear_split<128, ACT>(a, sms, st);
+  const int pairs = resident_pairs<ACT>(sms);
   if (pairs <= 0) return ITTT_ERR_CUDA;
   const long long n_tiles = cdiv(a.N, 256);
   if (n_tiles * cdiv(a.M, 256) * 4 >= pairs * 3) {
@@ -219,10 +223,26 @@ ittt_status linear_bf16(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
         best = mt;
       }
     }
-    return linear_pairs(a, best, pairs, st);
+    return linear_pairs<ACT>(a, best, pairs, st);
   }
-  if (cdiv(a.N, 128) * cdiv(a.M, 128) * 8 < sms) return linear_split<64>(a, sms, st);
-  return linear_split<128>(a, sms, st);
+  if (cdiv(a.N, 128) * cdiv(a.M, 128) * 8 < sms) return linear_split<64, ACT>(a, sms, st);
+  return linear_split<128, ACT>(a, sms, st);
+}
+
+template <int ACT>
+ittt_status linear_typed(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) { return linear_bf16<ACT>(a, st); }
+template <int ACT>
+ittt_status linear_typed(const LinearArgs<float>& a, cudaStream_t st) { return linear_f32<ACT>(a, st); }
+
+template <typename T_>
+ittt_status linear_by_act(const LinearArgs<T_>& a, cudaStream_t st) {
+  switch (a.act) {
+    case ITTT_ACT_RELU: return linear_typed<ITTT_ACT_RELU>(a, st);
+    case ITTT_ACT_SILU: return linear_typed<ITTT_ACT_SILU>(a, st);
+    case ITTT_ACT_GELU: return linear_typed<ITTT_ACT_GELU>(a, st);
+    case ITTT_ACT_GELU_TANH: return linear_typed<ITTT_ACT_GELU_TANH>(a, st);
+    default: return linear_typed<ITTT_ACT_NONE>(a, st);
+  }
 }
 
 // ------------------------------------------------------------- causal conv
@@ -239,17 +259,37 @@ ittt_status validate_conv(const ittt_conv_problem* p) {
 }
 
 // Single tokens: one token a thread; else runs of eight.
-template <typename T_, int KT>
+template <typename T_, int V, int KT, int ACT>
 ittt_status causal_conv_vec(const CausalConvArgs<T_>& a, cudaStream_t st) {
-  const long long groups = a.d / (16 / int(sizeof(T_))), run = a.T == 1 ? 1 : 8;
-  const long long runs = cdiv(a.T, run), total = a.B * runs * groups;
+  const long long groups = a.d / V, runs = cdiv(a.T, a.T == 1 ? 1 : 8), total = a.B * runs * groups;
   if (total >= (1ll << 32) - 128) return ITTT_ERR_UNSUPPORTED;
   const dim3 grid(unsigned(cdiv(total, 128)));
   if (a.T == 1)
-    return launch_pdl(causal_conv_vec_kernel<T_, KT, 1>, grid, dim3(128), st, a, unsigned(total),
-                      unsigned(groups), unsigned(runs));
-  return launch_pdl(causal_conv_vec_kernel<T_, KT, 8>, grid, dim3(128), st, a, unsigned(total),
-                    unsigned(groups), unsigned(runs));
+    return launch_pdl(causal_conv_vec_kernel<T_, V, KT, 1, ACT>, grid, dim3(128), st, a,
+                      unsigned(total), unsigned(groups), unsigned(runs));
+  return launch_pdl(causal_conv_vec_kernel<T_, V, KT, 8, ACT>, grid, dim3(128), st, a,
+                    unsigned(total), unsigned(groups), unsigned(runs));
+}
+
+template <typename T_, int V, int KT>
+ittt_status causal_conv_act(const CausalConvArgs<T_>& a, cudaStream_t st) {
+  if (a.act == ITTT_ACT_SILU) return causal_conv_vec<T_, V, KT, ITTT_ACT_SILU>(a, st);
+  if (a.act == ITTT_ACT_NONE) return causal_conv_vec<T_, V, KT, ITTT_ACT_NONE>(a, st);
+  return causal_conv_vec<T_, V, KT, -1>(a, st);  // by a.act
+}
+
+template <typename T_, int V>
+ittt_status causal_conv_taps(const CausalConvArgs<T_>& a, cudaStream_t st) {
+  switch (a.k) {
+    case 1: return causal_conv_act<T_, V, 1>(a, st);
+    case 2: return causal_conv_act<T_, V, 2>(a, st);
+    case 3: return causal_conv_act<T_, V, 3>(a, st);
+    case 4: return causal_conv_act<T_, V, 4>(a, st);
+    case 5: return causal_conv_act<T_, V, 5>(a, st);
+    case 6: return causal_conv_act<T_, V, 6>(a, st);
+    case 7: return causal_conv_act<T_, V, 7>(a, st);
+    default: return causal_conv_act<T_, V, 8>(a, st);
+  }
 }
 
 template <typename T_>
@@ -272,20 +312,9 @@ ittt_status causal_conv_launch(const ittt_conv_problem* p, const void* X, const 
   a.k = p->k;
   a.act = p->act;
   constexpr int V = 16 / int(sizeof(T_));
-  const bool vec = p->k <= 8 && p->d % V == 0 && a.ldx % V == 0 && a.ldy % V == 0 && aligned16(X) &&
+  const bool vec = p->d % V == 0 && a.ldx % V == 0 && a.ldy % V == 0 && aligned16(X) &&
                    aligned16(w) && aligned16(Y) && aligned16(a.state_in) && aligned16(a.state_out);
-  if (vec) {
-    switch (p->k) {
-      case 1: return causal_conv_vec<T_, 1>(a, st);
-      case 2: return causal_conv_vec<T_, 2>(a, st);
-      case 3: return causal_conv_vec<T_, 3>(a, st);
-      case 4: return causal_conv_vec<T_, 4>(a, st);
-      case 5: return causal_conv_vec<T_, 5>(a, st);
-      case 6: return causal_conv_vec<T_, 6>(a, st);
-      case 7: return causal_conv_vec<T_, 7>(a, st);
-      default: return causal_conv_vec<T_, 8>(a, st);
-    }
-  }
+  if (p->k <= 8) return vec ? causal_conv_taps<T_, V>(a, st) : causal_conv_taps<T_, 1>(a, st);
   const long long rest = p->T - (p->k - 1);
   const long long gy = 1 + (rest > 0 ? cdiv(rest, 16) : 0);
   if (gy > 65535) return ITTT_ERR_UNSUPPORTED;
@@ -394,11 +423,27 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
 }
 
 template <typename T_>
-ittt_status scan_short(const ScanArgs<T_>& a, cudaStream_t st) {
+ittt_status scan_short(const ScanArgs<T_>& a, int sms, cudaStream_t st) {
   const int npl = a.N <= 128 ? 4 : 8;
   int lanes = 1;
   while (lanes * npl < a.N) lanes *= 2;
   const int aligned = aligned16(a.A) && aligned16(a.state_in) && aligned16(a.state_out);
+  if (a.T == 1 && a.N <= 128) {
+    // four sequences a thread where that leaves 8 warps an SM, else one
+    constexpr uintptr_t quad = 4 * sizeof(T_) - 1;
+    const int vec_f32 = aligned && a.N % 4 == 0;
+    const int vec_bc = a.N % 4 == 0 && a.ldb % 4 == 0 && a.ldc % 4 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(a.Bm) | reinterpret_cast<uintptr_t>(a.Cm)) & quad) == 0;
+    const long long threads = (long long)a.d * lanes;
+#ifndef TOKSEQ
+#define TOKSEQ 2
+#endif
+    if (TOKSEQ > 1 && cdiv(a.B, TOKSEQ) * threads >= 256ll * sms)
+      return launch_pdl(scan_token_kernel<T_, TOKSEQ>, dim3(unsigned(cdiv(cdiv(a.B, TOKSEQ) * threads, 128))),
+                        dim3(128), st, a, lanes, vec_f32, vec_bc);
+    return launch_pdl(scan_token_kernel<T_, 1>, dim3(unsigned(cdiv(a.B * threads, 128))), dim3(128), st,
+                      a, lanes, vec_f32, vec_bc);
+  }
   const dim3 grid(unsigned(cdiv((long long)a.B * a.d * lanes, 128)));
   if (npl == 4) return launch_pdl(scan_serial_kernel<T_, 4>, grid, dim3(128), st, a, lanes, aligned);
   return launch_pdl(scan_serial_kernel<T_, 8>, grid, dim3(128), st, a, lanes, aligned);
@@ -422,7 +467,7 @@ ittt_status scan_launch(const ittt_scan_problem* p, const ScanArgs<T_>& a, void*
   const ScanCut c = scan_cut(p, sms);
   if (c.total && (!workspace || workspace_bytes < c.total)) return ITTT_ERR_WORKSPACE;
   if (c.total && !aligned16(workspace)) return ITTT_ERR_UNSUPPORTED;
-  if (c.short_call) return scan_short(a, st);
+  if (c.short_call) return scan_short(a, sms, st);
   char* ws = static_cast<char*>(workspace);
   ScanPlan pl{};
   pl.blocks = c.blocks;
@@ -469,9 +514,9 @@ ittt_status ittt_linear(const ittt_linear_problem* p, const void* X, const void*
     return s;
   if (p->dtype == ITTT_BF16) {
     if (!aligned16(X) || !aligned16(W)) return ITTT_ERR_UNSUPPORTED;
-    return linear_bf16(linear_args<__nv_bfloat16>(p, X, W, bias, residual, Y), as_stream(stream));
+    return linear_by_act(linear_args<__nv_bfloat16>(p, X, W, bias, residual, Y), as_stream(stream));
   }
-  return linear_f32(linear_args<float>(p, X, W, bias, residual, Y), as_stream(stream));
+  return linear_by_act(linear_args<float>(p, X, W, bias, residual, Y), as_stream(stream));
 }
 
 ittt_status ittt_causal_conv(const ittt_conv_problem* p, const void* X, const void* conv_kernel,

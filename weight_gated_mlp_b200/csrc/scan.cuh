@@ -5,8 +5,10 @@
 // One exponential per state element and token is the largest cost (the unit that
 // computes it takes 16 a clock and SM), so no kernel computes one twice.
 //
-//   scan_serial_kernel  short calls and single tokens: lanes over the state, four
-//       or eight elements a lane, token after token.  Bound by the state's bytes.
+//   scan_token_kernel   single tokens: lanes over the state, several sequences a
+//       thread.  Bound by the state's bytes.
+//   scan_serial_kernel  short calls: lanes over the state, four or eight elements a
+//       lane, token after token.
 //   scan_chunk_kernel   prompts: 8 channels a CTA, 256 tokens at a time.  A
 //       thread owns two neighbouring channels and 8 consecutive tokens, a warp two
 //       channels and the whole chunk.  For four state elements at once a thread runs
@@ -159,6 +161,106 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, 
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
         if (i < live) a.state_out[w * a.N + n0 + i] = h[i];
+    }
+  }
+}
+
+// Four values of a row.
+__device__ __forceinline__ void load_quad(const __nv_bfloat16* p, bool vec, int live, float (&v)[4]) {
+  if (vec) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+    v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < live ? __bfloat162float(p[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void load_quad(const float* p, bool vec, int live, float (&v)[4]) {
+  if (vec) {
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < live ? p[i] : 0.f;
+  }
+}
+
+// Single tokens (N <= 128): four state elements a lane of one channel, for SEQ
+// sequences at once, so that A is read once for them and SEQ times as many bytes
+// of state are in flight.  Bound by reading and writing the state.
+template <typename T_, int SEQ>
+__global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs<T_> a, int lanes, int vec_f32,
+                                                         int vec_bc) {
+  grid_dependency_wait();
+  const long long gid = (blockIdx.x * 128ll + threadIdx.x) / lanes;
+  const int sub = threadIdx.x & (lanes - 1);
+  const int batches = (a.B + SEQ - 1) / SEQ;
+  // every thread of a warp stays for the shuffles; those past the end repeat the last channel
+  const bool real = gid < (long long)batches * a.d;
+  const long long w = real ? gid : (long long)batches * a.d - 1;
+  const int b0 = static_cast<int>(w / a.d) * SEQ, c = static_cast<int>(w % a.d);
+  const int g = c / (a.d / a.G);
+  const int n0 = sub * 4, live = min(4, a.N - n0);
+  const bool vf = vec_f32 && live == 4, vb = vec_bc && live == 4;
+  const long long cn = (long long)c * a.N + n0, gn = (long long)g * a.N + n0;
+  float A2[4] = {}, h[SEQ][4] = {}, bq[SEQ][4] = {}, cq[SEQ][4] = {}, u[SEQ], s[SEQ], z[SEQ];
+  // every load before any arithmetic (rows past the batch repeat the last one)
+  long long row[SEQ];
+#pragma unroll
+  for (int i = 0; i < SEQ; ++i) row[i] = min(b0 + i, a.B - 1);
+  if (live > 0) {
+#pragma unroll
+    for (int i = 0; i < SEQ; ++i)
+      if (a.state_in) load_quad(a.state_in + row[i] * a.d * a.N + cn, vf, live, h[i]);
+    load_quad(a.A + cn, vf, live, A2);
+#pragma unroll
+    for (int i = 0; i < SEQ; ++i) {
+      load_quad(a.Bm + row[i] * a.ldb + gn, vb, live, bq[i]);
+      load_quad(a.Cm + row[i] * a.ldc + gn, vb, live, cq[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < SEQ; ++i) {
+    u[i] = to_f32(a.U[row[i] * a.ldu + c]);
+    s[i] = to_f32(a.delta[row[i] * a.ldt + c]);
+    z[i] = a.Z ? to_f32(a.Z[row[i] * a.ldz + c]) : 0.f;
+  }
+  const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
+  const float skip = a.D ? a.D[c] : 0.f;
+#pragma unroll
+  for (int i = 0; i < SEQ; ++i) {
+    const bool in = real && b0 + i < a.B;
+    const bool on = in && (!a.lengths || a.lengths[row[i]] > 0);
+    float y = 0.f;
+    if (on) {
+      float st = s[i] + bias;
+      if (a.softplus) st = softplus_f32(st);
+      const float su = st * u[i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float next = fmaf(exp2_approx(st * (A2[j] * kLog2e)), h[i][j], su * bq[i][j]);
+        if (j < live) {
+          h[i][j] = next;
+          y = fmaf(next, cq[i][j], y);
+        }
+      }
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    if (on && sub == 0) {
+      if (a.D) y = fmaf(skip, u[i], y);
+      if (a.Z) y *= silu_fast(z[i]);
+      a.Y[row[i] * a.ldy + c] = from_f32<T_>(y);
+    }
+    if (a.state_out && in && live > 0) {  // an empty sequence passes its state through
+      float* p = a.state_out + row[i] * a.d * a.N + cn;
+      if (vf) {
+        *reinterpret_cast<float4*>(p) = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < live) p[j] = h[i][j];
+      }
     }
   }
 }

@@ -25,6 +25,7 @@ namespace ittt {
 
 // Outputs (m, n) for m in [m0, m0 + count) of one lane's column n: acc holds the
 // sums of 32 rows of X.
+template <int ACT>
 __device__ __forceinline__ void linear_store32(const LinearArgs<__nv_bfloat16>& a,
                                                const uint32_t (&acc)[32], int n, int m0, int count,
                                                float bias) {
@@ -39,7 +40,7 @@ __device__ __forceinline__ void linear_store32(const LinearArgs<__nv_bfloat16>& 
     }
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      float v = activate(__uint_as_float(acc[j]) + bias, a.act);
+      float v = activate<ACT>(__uint_as_float(acc[j]) + bias);
       if (r) v += res[j];
       y[j * a.ldy] = __float2bfloat16_rn(v);
     }
@@ -47,7 +48,7 @@ __device__ __forceinline__ void linear_store32(const LinearArgs<__nv_bfloat16>& 
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       if (j < count) {
-        float v = activate(__uint_as_float(acc[j]) + bias, a.act);
+        float v = activate<ACT>(__uint_as_float(acc[j]) + bias);
         if (r) v += __bfloat162float(r[j * a.ldr]);
         y[j * a.ldy] = __float2bfloat16_rn(v);
       }
@@ -55,19 +56,51 @@ __device__ __forceinline__ void linear_store32(const LinearArgs<__nv_bfloat16>& 
   }
 }
 
-// Shared-memory pipeline depth: about 100 KB, so that two CTAs share an SM and
-// enough bytes are in flight to cover HBM latency.
+// Shared-memory pipeline depth: up to 74 KB, so that three CTAs share an SM (two at
+// 128 rows) and enough bytes are in flight to cover HBM latency.
 template <int MT>
 struct SplitShape {
   static constexpr int STAGE_BYTES = 128 * 128 + MT * 128;  // 64 bf16 of 128 rows of W, MT of X
-  static constexpr int STAGES = MT <= 16 ? 6 : MT <= 32 ? 5 : MT <= 64 ? 4 : 3;
+  static constexpr int STAGES = MT <= 16 ? 4 : 3;
+  static constexpr int CTAS = MT <= 64 ? 3 : 2;  // an SM
   static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 256;
   static constexpr int TMEM_COLS = MT < 32 ? 32 : MT;
   static_assert(STAGES * STAGE_BYTES >= MT * 512, "the joined sums fit the pipeline's memory");
 };
 
-template <int MT>
-__global__ void __launch_bounds__(192)
+// One lane's column n of the rows rank, rank + S, ... of a tile: the S sums of each
+// row in rank order.  16 remote loads are in flight at once (one at a time, the
+// join of 64 rows took longer than the product's own pipeline).
+template <int MT, int S, int ACT>
+__device__ __forceinline__ void linear_join(const LinearArgs<__nv_bfloat16>& a, uint32_t mine, int rank,
+                                            int n, int m0, float bias) {
+  constexpr int ROWS = MT / S, BATCH = ROWS < 16 / S ? ROWS : 16 / S;
+#pragma unroll 1
+  for (int i0 = 0; i0 < ROWS; i0 += BATCH) {
+    const int c0 = rank + i0 * S;
+    if (m0 + c0 >= a.M) return;
+    float part[BATCH][S];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        part[i][s] = ld_shared_cluster_f32(cluster_addr(mine + (c0 + i * S) * 512u, s));
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const long long m = m0 + c0 + i * S;
+      if (m >= a.M) break;
+      float v = part[i][0];
+#pragma unroll
+      for (int s = 1; s < S; ++s) v += part[i][s];
+      v = activate<ACT>(v + bias);
+      if (a.residual) v += __bfloat162float(a.residual[m * a.ldr + n]);
+      a.Y[m * a.ldy + n] = __float2bfloat16_rn(v);
+    }
+  }
+}
+
+template <int MT, int ACT>
+__global__ void __launch_bounds__(192, SplitShape<MT>::CTAS)
     linear_split_kernel(const __grid_constant__ CUtensorMap tmW,
                         const __grid_constant__ CUtensorMap tmX,
                         const LinearArgs<__nv_bfloat16> a, int m_tiles, int num_kb,
@@ -188,7 +221,7 @@ __global__ void __launch_bounds__(192)
         __syncwarp();
         tmem_ld32(tbase + c0, v);
         tmem_ld_wait();
-        linear_store32(a, v, n, m0 + c0, min(MT - c0, a.M - (m0 + c0)), bias);
+        linear_store32<ACT>(a, v, n, m0 + c0, min(MT - c0, a.M - (m0 + c0)), bias);
       }
     }
   } else {
@@ -210,20 +243,10 @@ __global__ void __launch_bounds__(192)
     // rank i finishes the rows i, i + splits, ... of X
     if (ok && n < a.N) {
       const uint32_t mine = smem_u32(red) + static_cast<uint32_t>(r) * 4u;
-#pragma unroll 2
-      for (int c = rank; c < MT && m0 + c < a.M; c += splits) {
-        float part[8];
-#pragma unroll
-        for (int s = 0; s < 8; ++s)
-          part[s] = s < splits ? ld_shared_cluster_f32(cluster_addr(mine + c * 512u, s)) : 0.f;
-        float v = part[0];
-#pragma unroll
-        for (int s = 1; s < 8; ++s)
-          if (s < splits) v += part[s];
-        v = activate(v + bias, a.act);
-        const long long m = m0 + c;
-        if (a.residual) v += __bfloat162float(a.residual[m * a.ldr + n]);
-        a.Y[m * a.ldy + n] = __float2bfloat16_rn(v);
+      switch (splits) {
+        case 2: linear_join<MT, 2, ACT>(a, mine, rank, n, m0, bias); break;
+        case 4: linear_join<MT, 4, ACT>(a, mine, rank, n, m0, bias); break;
+        default: linear_join<MT, 8, ACT>(a, mine, rank, n, m0, bias); break;
       }
     }
     __syncwarp();
@@ -261,6 +284,7 @@ __device__ __forceinline__ void pair_decode(const PairTile& t, int u, int& mt, i
   mt = r / cols;
 }
 
+template <int ACT>
 __global__ void __launch_bounds__(192, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX,
@@ -415,7 +439,7 @@ __global__ void __launch_bounds__(192, 1)
         tmem_ld32(tbase + c0, v);  // past t.mt: columns of the slot that no row belongs to
         tmem_ld_wait();
         if (c0 + 32 >= t.mt) release(slot);
-        linear_store32(a, v, n, m0 + c0, min(t.mt - c0, a.M - (m0 + c0)), bias);
+        linear_store32<ACT>(a, v, n, m0 + c0, min(t.mt - c0, a.M - (m0 + c0)), bias);
       }
       slot ^= 1;
     }
