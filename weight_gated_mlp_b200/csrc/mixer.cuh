@@ -31,10 +31,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// x / (1 + e^-x) by the hardware's quotient (2 ulp).  Below -126 the value is
-// under 2^-174: 0 there, also at -inf, where the quotient would be NaN.
+// x / (1 + e^-x) by the hardware's quotient (2 ulp).  Below -126 the value is under
+// 2^-174, and the quotient by an infinite denominator gives the 0 it rounds to; the
+// argument is held there so that -inf gives 0 too (NaN stays NaN).
 __device__ __forceinline__ float silu_fast(float x) {
-  return x < -126.f ? 0.f : __fdividef(x, 1.f + exp2_approx(-kLog2e * x));
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x));
+  return __fdividef(x, 1.f + exp2_approx(-kLog2e * x));
 }
 
 // act(x) in fp32; at -inf the limit (0 for all but the identity).  A template
@@ -90,39 +92,45 @@ __device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, in
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
-// Bound by reading X and writing Y once.  A thread owns V neighbouring channels
-// (16 bytes; 1 where widths or alignment do not allow that) over RUN tokens: its RUN + KT - 1 rows are loaded before any
-// arithmetic, so that a warp keeps as many requests in flight, and a run
-// re-reads KT - 1 rows of the run before (from L2).
+// Bound by reading X and writing Y once, with the activation's two special-function
+// results a value close behind.  A thread owns V neighbouring channels (16 bytes; 1
+// where widths or alignment do not allow that) over `steps` times four tokens.  It
+// holds the KT - 1 rows before and four more, and asks for the next four before it
+// computes, so that loads and arithmetic overlap; a thread's first KT - 1 rows are
+// the only ones read twice.
 // The threads of token 0 also move the state: each reads its channels' state_in
-// (nobody else does: RUN >= KT - 1 for the runs behind) before it writes the same
+// (nobody else does: the others start at token 8 or later) before it writes the same
 // channels' state_out, so the two may be one buffer.
-template <typename T_, int V, int KT, int RUN, int ACT>
+template <typename T_, int V, int KT, int ACT>
 __global__ void __launch_bounds__(128) causal_conv_vec_kernel(const CausalConvArgs<T_> a,
                                                               unsigned total, unsigned groups,
-                                                              unsigned runs) {
+                                                              unsigned runs, int steps) {
   using Row = std::conditional_t<V == 1, T_, uint4>;
-  static_assert(RUN == 1 || RUN >= KT - 1, "only the first run reads state_in");
+  constexpr int R = 4;  // tokens a step
   grid_dependency_wait();
   const unsigned e = blockIdx.x * 128u + threadIdx.x;
   if (e >= total) return;
   const unsigned rest = e / groups;
   const int c = static_cast<int>(e - rest * groups) * V;
   const int b = static_cast<int>(rest / runs);
-  const int t0 = static_cast<int>(rest - unsigned(b) * runs) * RUN;
+  const int t0 = static_cast<int>(rest - unsigned(b) * runs) * steps * R;
   const int len = sequence_length(a.lengths, b, a.T);
   const T_* X = a.X + (long long)b * a.T * a.ldx + c;
   const T_* s_in = a.state_in ? a.state_in + (long long)b * (KT - 1) * a.d + c : nullptr;
-  auto row = [&](int t) -> Row {  // the inputs of token t >= -(KT - 1)
+  auto before = [&](int t) -> Row {  // the inputs of a token -(KT - 1) <= t < len
     if (t >= 0) return *reinterpret_cast<const Row*>(X + t * a.ldx);
     if (s_in) return *reinterpret_cast<const Row*>(s_in + (long long)(t + KT - 1) * a.d);
     return Row{};
   };
   if (t0 < len) {
-    Row rows[RUN + KT - 1];
+    const int t_end = min(len, t0 + steps * R);
+    Row rows[R + KT - 1], next[R];
+    const T_* xp = X + t0 * a.ldx;
 #pragma unroll
-    for (int i = 0; i < RUN + KT - 1; ++i)
-      rows[i] = t0 + i - (KT - 1) < len ? row(t0 + i - (KT - 1)) : Row{};
+    for (int i = 0; i < R; ++i)
+      next[i] = t0 + i < t_end ? *reinterpret_cast<const Row*>(xp + i * a.ldx) : Row{};
+#pragma unroll
+    for (int i = 0; i < KT - 1; ++i) rows[R + i] = before(t0 + i - (KT - 1));
     float w[KT][V], bias[V];
     {
       // the taps of V channels are V * KT contiguous elements
@@ -138,37 +146,49 @@ __global__ void __launch_bounds__(128) causal_conv_vec_kernel(const CausalConvAr
       for (int i = 0; i < V; ++i) bias[i] = a.bias ? to_f32(a.bias[c + i]) : 0.f;
     }
     T_* Y = a.Y + ((long long)b * a.T + t0) * a.ldy + c;
+#pragma unroll 1
+    for (int t = t0; t < t_end; t += R) {
 #pragma unroll
-    for (int t = 0; t < RUN; ++t) {
-      if (t0 + t < len) {
-        float y[V];
+      for (int i = 0; i < KT - 1; ++i) rows[i] = rows[R + i];
 #pragma unroll
-        for (int i = 0; i < V; ++i) y[i] = bias[i];
+      for (int i = 0; i < R; ++i) rows[KT - 1 + i] = next[i];
+      xp += R * a.ldx;
 #pragma unroll
-        for (int j = 0; j < KT; ++j) {
-          const T_* x = reinterpret_cast<const T_*>(&rows[t + j]);
+      for (int i = 0; i < R; ++i)
+        next[i] = t + R + i < t_end ? *reinterpret_cast<const Row*>(xp + i * a.ldx) : Row{};
 #pragma unroll
-          for (int i = 0; i < V; ++i) y[i] = fmaf(w[j][i], to_f32(x[i]), y[i]);
+      for (int r = 0; r < R; ++r) {
+        if (t + r < t_end) {
+          float y[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) y[i] = bias[i];
+#pragma unroll
+          for (int j = 0; j < KT; ++j) {
+            const T_* x = reinterpret_cast<const T_*>(&rows[r + j]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[i] = fmaf(w[j][i], to_f32(x[i]), y[i]);
+          }
+          Row out;
+          T_* o = reinterpret_cast<T_*>(&out);
+          if (ACT == ITTT_ACT_SILU) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[i] = silu_fast(y[i]);
+          } else if (ACT != ITTT_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) y[i] = activate_any(y[i], a.act);
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = from_f32<T_>(y[i]);
+          *reinterpret_cast<Row*>(Y + r * a.ldy) = out;
         }
-        Row out;
-        T_* o = reinterpret_cast<T_*>(&out);
-        if (ACT == ITTT_ACT_SILU) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) y[i] = silu_fast(y[i]);
-        } else if (ACT != ITTT_ACT_NONE) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) y[i] = activate_any(y[i], a.act);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = from_f32<T_>(y[i]);
-        *reinterpret_cast<Row*>(Y + t * a.ldy) = out;
       }
+      Y += R * a.ldy;
     }
   }
   if (KT > 1 && t0 == 0 && a.state_out) {
     Row keep[KT > 1 ? KT - 1 : 1];
 #pragma unroll
-    for (int j = 0; j < KT - 1; ++j) keep[j] = row(len - (KT - 1) + j);
+    for (int j = 0; j < KT - 1; ++j) keep[j] = before(len - (KT - 1) + j);
     T_* s_out = a.state_out + (long long)b * (KT - 1) * a.d + c;
 #pragma unroll
     for (int j = 0; j < KT - 1; ++j) *reinterpret_cast<Row*>(s_out + (long long)j * a.d) = keep[j];

@@ -213,17 +213,7 @@ ittt_status linear_bf16(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
   if (pairs <= 0) return ITTT_ERR_CUDA;
   const long long n_tiles = cdiv(a.N, 256);
   if (n_tiles * cdiv(a.M, 256) * 4 >= pairs * 3) {
-    int best = 256;
-    long long least = -1;
-    for (int mt = 256; mt >= 128; mt -= 32) {
-      // a wave of tiles costs its height, plus a part that does not shrink with it
-      const long long cost = cdiv(n_tiles * cdiv(a.M, mt), pairs) * (mt + 16);
-      if (least < 0 || cost < least) {
-        least = cost;
-        best = mt;
-      }
-    }
-    return linear_pairs<ACT>(a, best, pairs, st);
+    return linear_pairs<ACT>(a, 256, pairs, st);
   }
   if (cdiv(a.N, 128) * cdiv(a.M, 128) * 8 < sms) return linear_split<64, ACT>(a, sms, st);
   return linear_split<128, ACT>(a, sms, st);
@@ -258,17 +248,21 @@ ittt_status validate_conv(const ittt_conv_problem* p) {
   return ITTT_OK;
 }
 
-// Single tokens: one token a thread; else runs of eight.
+#ifndef CONV_STEPS
+#define CONV_STEPS 8
+#endif
+// Steps of four tokens a thread: 8 while that leaves every SM 16 warps, down to 2.
 template <typename T_, int V, int KT, int ACT>
 ittt_status causal_conv_vec(const CausalConvArgs<T_>& a, cudaStream_t st) {
-  const long long groups = a.d / V, runs = cdiv(a.T, a.T == 1 ? 1 : 8), total = a.B * runs * groups;
+  const int sms = num_sms();
+  if (sms <= 0) return ITTT_ERR_CUDA;
+  const long long groups = a.d / V;
+  int steps = CONV_STEPS;
+  while (steps > 2 && a.B * cdiv(a.T, 4 * steps) * groups < 512ll * sms) steps /= 2;
+  const long long runs = cdiv(a.T, 4 * steps), total = a.B * runs * groups;
   if (total >= (1ll << 32) - 128) return ITTT_ERR_UNSUPPORTED;
-  const dim3 grid(unsigned(cdiv(total, 128)));
-  if (a.T == 1)
-    return launch_pdl(causal_conv_vec_kernel<T_, V, KT, 1, ACT>, grid, dim3(128), st, a,
-                      unsigned(total), unsigned(groups), unsigned(runs));
-  return launch_pdl(causal_conv_vec_kernel<T_, V, KT, 8, ACT>, grid, dim3(128), st, a,
-                    unsigned(total), unsigned(groups), unsigned(runs));
+  return launch_pdl(causal_conv_vec_kernel<T_, V, KT, ACT>, dim3(unsigned(cdiv(total, 128))), dim3(128),
+                    st, a, unsigned(total), unsigned(groups), unsigned(runs), steps);
 }
 
 template <typename T_, int V, int KT>

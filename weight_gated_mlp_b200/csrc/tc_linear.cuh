@@ -426,6 +426,10 @@ __global__ void __launch_bounds__(192, 1)
       const int n = nt * 256 + static_cast<int>(rank) * 128 + r;
       const int m0 = mt * t.mt;
       const float bias = (a.bias && n < a.N) ? __bfloat162float(a.bias[n]) : 0.f;
+      // this warp's 64 bytes of the tile's residual rows come into L2 during the main loop
+      if (a.residual && n - lane < a.N)
+        for (int i = lane; i < t.mt && m0 + i < a.M; i += 32)
+          prefetch_l2(a.residual + (long long)(m0 + i) * a.ldr + n - lane);
       const bool ok = mbar_wait(&tfull[slot], count[slot] & 1, wc);
       __syncwarp();
       if (!ok) break;
