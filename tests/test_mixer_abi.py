@@ -111,7 +111,7 @@ def test_scan_pointers(lib):
 
 def test_rows_of_a_view():
     """The row stride of dense tensors, column slices, single tokens; others are refused."""
-    rows = lambda t: ittt._rows(t, "t", t.shape, t.dtype, -1)[1]  # noqa: E731
+    rows = lambda t: ittt._marshal().row_stride(t, 1)  # noqa: E731
     base = torch.zeros(3, 5, 24)
     assert rows(base) == 0
     assert rows(base[:, :, 8:16]) == 24
@@ -122,7 +122,13 @@ def test_rows_of_a_view():
                 base[:, :1].expand(3, 5, 24), base[:1].expand(3, 5, 24), base[:1, :1].expand(3, 5, 24)):
         with pytest.raises(ValueError, match="column slice"):
             rows(bad)
-    rows(base[:1, ::2])                           # one sequence, every other row: rows 48 apart
+    assert rows(base[:1, ::2]) == 48              # one sequence, every other row
+    four = torch.zeros(3, 5, 4, 6)                # the groups of a token side by side
+    row4 = lambda t: ittt._marshal().row_stride(t, 2)  # noqa: E731
+    assert row4(four) == 0 and row4(four[:, :, 1:3]) == 24 and row4(four[:, :, 2:3]) == 24
+    for bad in (four[:, :, ::2], four[..., :3], four.transpose(2, 3)):
+        with pytest.raises(ValueError, match="side by side"):
+            row4(bad)
 
 
 def test_binding_refusals():
@@ -141,4 +147,6 @@ def test_binding_refusals():
         ittt.selective_scan(torch.zeros(1, 4, 8), torch.zeros(1, 4, 8), torch.zeros(8, 2),
                             torch.zeros(1, 4, 2), torch.zeros(1, 4, 2))
     with pytest.raises(ValueError, match="activation"):
-        ittt._act_of("swish")
+        ittt.linear(x, w, act="swish")
+    with pytest.raises(TypeError, match="tensor"):
+        ittt.linear([1.0], w)

@@ -1,7 +1,8 @@
 """Python binding of ``libittt.so``, the B200 (sm_100a) In-Place TTT fast-weight MLP layer.
 
-Argument marshalling only: every step of the computation runs in the CUDA
-kernels behind the C ABI of ``include/ittt.h``.  torch supplies device
+Argument marshalling only (ctypes, and a compiled module for the short calls
+around the layer): every step of the computation runs in the CUDA kernels
+behind the C ABI of ``include/ittt.h``.  torch supplies device
 memory and streams.  The library must have been built
 (``python -m weight_gated_mlp_b200._build``); importing this module without
 it raises, and there is no CPU fallback.
@@ -10,7 +11,6 @@ it raises, and there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from typing import Optional, Tuple
 
@@ -443,84 +443,30 @@ class Decoder:
 
 # ------------------------------------------------------------ around the layer
 
-def _switch_to(t) -> Tuple[int, int]:
-    """(device of t, device to switch back to or -1): makes t's device current."""
-    if not t.is_cuda:
-        raise ValueError("the operands must be CUDA tensors")
-    torch = _torch()
-    dev, before = t.get_device(), torch._C._cuda_getDevice()
-    if dev == before:
-        return dev, -1
-    torch.cuda.set_device(dev)
-    return dev, before
+# These calls are marshalled by a compiled module (csrc/marshal.cpp) instead of
+# ctypes: a decode step makes several of them a token, and each kernel is shorter
+# than Python's checks of its tensors.
+
+_marshal_module = None
 
 
-def _stream_on(dev: int, stream) -> Optional[int]:
-    """The raw handle of a stream, or of device dev's current one."""
-    if stream is not None:
-        return int(stream.cuda_stream) or None
-    return _torch()._C._cuda_getCurrentRawStream(dev) or None
+def _marshal():
+    """The compiled marshalling module, bound to the loaded library."""
+    global _marshal_module
+    if _marshal_module is None:
+        import importlib.util
 
-
-def _misfit(t, name: str, shape, dtype, dev: int) -> None:
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _same(t, name: str, shape, dtype, dev: int) -> int:
-    """The address of a dense tensor of this shape, type and device."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _misfit(t, name, shape, dtype, dev)
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _rows(t, name: str, shape, dtype, dev: int) -> Tuple[int, int]:
-    """(address, elements between rows) of a [..., width] tensor whose rows are a
-    fixed distance apart (dense, or a column slice of a dense tensor)."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _misfit(t, name, shape, dtype, dev)
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    strides = t.stride()
-    if len(strides) == 3 and strides[2] == 1 and strides[1] >= shape[2] and \
-            strides[0] == strides[1] * shape[1]:
-        return t.data_ptr(), strides[1]
-    width = shape[-1]
-    ld, step, ok = None, 0, strides[-1] == 1 or width == 1
-    for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-        if size == 1:
-            continue
-        if ld is None:
-            ld = step = stride
-        ok = ok and stride == step
-        step *= size
-    ld = width if ld is None else ld
-    if not ok or ld < width:
-        raise ValueError(f"{name} must be dense, or a column slice of a dense tensor "
-                         f"(shape {tuple(t.shape)}, strides {t.stride()})")
-    return t.data_ptr(), ld
-
-
-def _used_on(stream, *tensors) -> None:
-    """Tensors made here for work on another stream than the current one: their
-    memory is not given out again before that work is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-
-
-def _new_like(t, other, shape):
-    """A dense tensor of this shape, of t's type where t has that shape and is
-    dense (the cheaper call), else of other's."""
-    if t is not None and t.shape == shape and t.is_contiguous():
-        return _torch().empty_like(t)
-    return other.new_empty(shape)
+        _torch()       # the module links against torch's libraries
+        load_library()
+        path = os.path.join(PKG, "_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"marshalling module missing: {path} (run python -m weight_gated_mlp_b200._build)")
+        spec = importlib.util.spec_from_file_location(__name__ + "._marshal", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(_lib._name, IttTError)
+        _marshal_module = module
+    return _marshal_module
 
 
 def _act_of(act: str) -> int:
@@ -528,21 +474,6 @@ def _act_of(act: str) -> int:
     if code is None:
         raise ValueError(f"unknown activation {act!r}, expected one of {sorted(_ACTS)}")
     return code
-
-
-def _grouped_rows(t, name: str, shape, dtype, dev: int) -> Tuple[int, int]:
-    """_rows of [B, T, G, N], a token's G N values being neighbours."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _misfit(t, name, shape, dtype, dev)
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    B, T, G, N = shape
-    sb, st, sg, sn = t.stride()
-    if (N > 1 and sn != 1) or (G > 1 and sg != N):
-        raise ValueError(f"the groups of {name} must stand side by side (strides {t.stride()})")
-    if sb == st * T and st >= G * N:
-        return t.data_ptr(), st
-    return _rows(t.as_strided((B, T, G * N), (sb, st, 1)), name, (B, T, G * N), dtype, dev)
 
 
 def linear(X, W, bias=None, residual=None, act: str = "none", out=None, stream=None):
@@ -553,36 +484,7 @@ def linear(X, W, bias=None, residual=None, act: str = "none", out=None, stream=N
     same tensor; all of one dtype (bf16 with K % 8 == 0, or fp32).  act: "none",
     "relu", "silu", "gelu" or "gelu_tanh".
     """
-    dt = X.dtype
-    code = BF16 if _dtype_name(X) == "bf16" else F32
-    if X.dim() < 1 or W.dim() != 2:
-        raise ValueError("X must have shape [..., K] and W [N, K]")
-    N, K = W.shape
-    x_shape = X.shape
-    if x_shape[-1] != K:
-        raise ValueError(f"X has {x_shape[-1]} columns, W {K}")
-    shape = (*x_shape[:-1], N)
-    dev, before = _switch_to(X)
-    try:
-        made = None
-        if out is None:
-            out = made = X.new_empty(shape)
-            y, ldy = out.data_ptr(), 0
-        else:
-            y, ldy = _rows(out, "out", shape, dt, dev)
-        x, ldx = _rows(X, "X", x_shape, dt, dev)
-        r, ldr = _rows(residual, "residual", shape, dt, dev) if residual is not None else (None, 0)
-        w = _same(W, "W", (N, K), dt, dev)
-        b = _same(bias, "bias", (N,), dt, dev) if bias is not None else None
-        if stream is not None:
-            _used_on(stream, made)
-        p = LinearProblem(math.prod(shape[:-1]), N, K, ldx, ldr, ldy, code, _act_of(act))
-        _check(load_library().ittt_linear(ctypes.byref(p), x, w, b, r, y, _stream_on(dev, stream)),
-               "ittt_linear")
-    finally:
-        if before >= 0:
-            _torch().cuda.set_device(before)
-    return out
+    return (_marshal_module or _marshal()).linear(X, W, bias, residual, _act_of(act), out, stream)
 
 
 def causal_conv(X, conv_kernel, bias=None, act: str = "none", state=None, lengths=None, out=None,
@@ -598,41 +500,8 @@ def causal_conv(X, conv_kernel, bias=None, act: str = "none", state=None, length
     sequence of a padded batch; rows of Y behind them are left as they were
     (what ``out`` held).
     """
-    dt = X.dtype
-    code = BF16 if _dtype_name(X) == "bf16" else F32
-    if X.dim() != 3 or conv_kernel.dim() != 2:
-        raise ValueError("X must have shape [B, T, d] and conv_kernel [d, k]")
-    shape = X.shape
-    B, T, d = shape
-    k = conv_kernel.shape[1]
-    dev, before = _switch_to(X)
-    try:
-        made = made_state = None
-        if out is None:
-            # rows behind a sequence's end are not written: they come out as zeros
-            out = made = _new_like(X, X, shape) if lengths is None else X.new_zeros(shape)
-            y, ldy = out.data_ptr(), 0
-        else:
-            y, ldy = _rows(out, "out", shape, dt, dev)
-        if state_out is None:
-            state_out = made_state = _new_like(state, X, (B, max(k - 1, 0), d))
-            so = state_out.data_ptr()
-        else:
-            so = _same(state_out, "state_out", (B, k - 1, d), dt, dev)
-        x, ldx = _rows(X, "X", shape, dt, dev)
-        w = _same(conv_kernel, "conv_kernel", (d, k), dt, dev)
-        b = _same(bias, "bias", (d,), dt, dev) if bias is not None else None
-        s = _same(state, "state", (B, k - 1, d), dt, dev) if state is not None else None
-        n = _same(lengths, "lengths", (B,), _torch().int32, dev) if lengths is not None else None
-        if stream is not None:
-            _used_on(stream, made, made_state)
-        p = ConvProblem(B, T, d, ldx, ldy, k, code, _act_of(act), 0)
-        _check(load_library().ittt_causal_conv(ctypes.byref(p), x, w, b, s, n, y, so,
-                                               _stream_on(dev, stream)), "ittt_causal_conv")
-    finally:
-        if before >= 0:
-            _torch().cuda.set_device(before)
-    return out, state_out
+    return (_marshal_module or _marshal()).causal_conv(X, conv_kernel, bias, _act_of(act), state, lengths,
+                                                       out, state_out, stream)
 
 
 def selective_scan(U, delta, A, Bm, Cm, D=None, Z=None, dt_bias=None, dt_softplus: bool = False,
@@ -648,63 +517,9 @@ def selective_scan(U, delta, A, Bm, Cm, D=None, Z=None, dt_bias=None, dt_softplu
     before the first token (None: zeros); state_out may be the same tensor.  T =
     1 is a decode step.  lengths: int32 [B], as for ``causal_conv``.
     """
-    dt = U.dtype
-    code = BF16 if _dtype_name(U) == "bf16" else F32
-    grouped = Bm.dim() == 4
-    if U.dim() != 3 or A.dim() != 2 or Bm.dim() not in (3, 4):
-        raise ValueError("U must have shape [B, T, d], A [d, N], Bm and Cm [B, T, N] or [B, T, G, N]")
-    shape = U.shape
-    B, T, d = shape
-    N = A.shape[1]
-    G = Bm.shape[2] if grouped else 1
-    f32 = _torch().float32
-    dev, before = _switch_to(U)
-    try:
-        made = made_state = scratch = None
-        if out is None:
-            out = made = _new_like(U, U, shape) if lengths is None else U.new_zeros(shape)
-            y, ldy = out.data_ptr(), 0
-        else:
-            y, ldy = _rows(out, "out", shape, dt, dev)
-        if state_out is None:
-            state_out = made_state = _new_like(state, A, (B, d, N))
-            so = state_out.data_ptr()
-        else:
-            so = _same(state_out, "state_out", (B, d, N), f32, dev)
-        u, ldu = _rows(U, "U", shape, dt, dev)
-        dl, ldt = _rows(delta, "delta", shape, dt, dev)
-        z, ldz = _rows(Z, "Z", shape, dt, dev) if Z is not None else (None, 0)
-        if grouped:
-            bm, ldb = _grouped_rows(Bm, "Bm", (B, T, G, N), dt, dev)
-            cm, ldc = _grouped_rows(Cm, "Cm", (B, T, G, N), dt, dev)
-        else:
-            bm, ldb = _rows(Bm, "Bm", (B, T, N), dt, dev)
-            cm, ldc = _rows(Cm, "Cm", (B, T, N), dt, dev)
-        a = _same(A, "A", (d, N), f32, dev)
-        sk = _same(D, "D", (d,), f32, dev) if D is not None else None
-        db = _same(dt_bias, "dt_bias", (d,), f32, dev) if dt_bias is not None else None
-        s = _same(state, "state", (B, d, N), f32, dev) if state is not None else None
-        n = _same(lengths, "lengths", (B,), _torch().int32, dev) if lengths is not None else None
-        p = ScanProblem(B, T, d, ldu, ldt, ldb, ldc, ldz, ldy, N, G, code,
-                        SCAN_SOFTPLUS if dt_softplus else 0)
-        ref = ctypes.byref(p)
-        need = ctypes.c_size_t(0)
-        lib = load_library()
-        _check(lib.ittt_selective_scan_workspace_size(ref, ctypes.byref(need)),
-               "ittt_selective_scan_workspace_size")
-        need, ws = need.value, None
-        if need:
-            if workspace is None or workspace.numel() < need:
-                workspace = scratch = U.new_empty(need, dtype=_torch().uint8)
-            ws = workspace.data_ptr()
-        if stream is not None:
-            _used_on(stream, made, made_state, scratch)
-        _check(lib.ittt_selective_scan(ref, u, dl, a, bm, cm, sk, db, z, s, n, y, so, ws, need,
-                                       _stream_on(dev, stream)), "ittt_selective_scan")
-    finally:
-        if before >= 0:
-            _torch().cuda.set_device(before)
-    return out, state_out
+    return (_marshal_module or _marshal()).selective_scan(
+        U, delta, A, Bm, Cm, D, Z, dt_bias, SCAN_SOFTPLUS if dt_softplus else 0, state, lengths, out,
+        state_out, workspace, stream)
 
 
 # ------------------------------------------------------------ context parallel

@@ -1,8 +1,11 @@
-"""Build of the CUDA library ``libittt.so`` (sm_100a) next to this file.
+"""Build of the CUDA library ``libittt.so`` (sm_100a) and of the argument
+marshalling module ``_marshal.so`` next to this file.
 
 ``python -m weight_gated_mlp_b200._build`` compiles ``csrc/api.cu`` (which
 includes every kernel header) with nvcc into a shared library exporting the
 C ABI of ``include/ittt.h``.  The CUDA runtime is linked statically.
+``csrc/marshal.cpp`` (g++, torch's headers) becomes the Python module through
+which the operators around the layer are called.
 """
 
 from __future__ import annotations
@@ -11,13 +14,16 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libittt.so")
 SOURCES = [os.path.join(PKG, "csrc", "api.cu")]
-DEPS = [os.path.join(PKG, "csrc", n) for n in sorted(os.listdir(os.path.join(PKG, "csrc")))] + [
-    os.path.join(ROOT, "include", "ittt.h")]
+DEPS = [os.path.join(PKG, "csrc", n) for n in sorted(os.listdir(os.path.join(PKG, "csrc")))
+        if not n.endswith(".cpp")] + [os.path.join(ROOT, "include", "ittt.h")]
+MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_SOURCE = os.path.join(PKG, "csrc", "marshal.cpp")
 
 
 def nvcc_path() -> str:
@@ -36,23 +42,48 @@ def command(out: str = LIB, verbose_ptxas: bool = False) -> list:
     return cmd
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def marshal_command(out: str = MARSHAL) -> list:
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    lib = os.path.join(base, "lib")
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
+            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+            "-o", out, MARSHAL_SOURCE, "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+
+
+def newer(target: str, sources) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in DEPS if os.path.exists(p))
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in sources if os.path.exists(p))
+
+
+def up_to_date() -> bool:
+    return newer(LIB, DEPS)
+
+
+def run(cmd: list, target: str, what: str):
+    """Run a compiler command that writes target + ".tmp", then move it into place."""
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n" + res.stdout + res.stderr)
+    os.replace(target + ".tmp", target)
+    return res
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    tmp = LIB + ".tmp"
-    res = subprocess.run(command(tmp, verbose_ptxas), capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + res.stdout + res.stderr)
-    if verbose_ptxas:
-        sys.stderr.write(res.stderr)
-    os.replace(tmp, LIB)
+    if force or not newer(MARSHAL, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "ittt.h")]):
+        run(marshal_command(MARSHAL + ".tmp"), MARSHAL, "g++")
+    if force or not up_to_date():
+        res = run(command(LIB + ".tmp", verbose_ptxas), LIB, "nvcc")
+        if verbose_ptxas:
+            sys.stderr.write(res.stderr)
     return LIB
 
 
