@@ -126,6 +126,35 @@ __device__ __forceinline__ float4 f32_quad(const float* p, long long ld, int r, 
   return v;
 }
 
+// The rows rank, rank + S, ... of a tile: the S sums of each value in rank order, 32
+// remote loads in flight.
+template <int ACT, int BM, int BN, int TH, int S>
+__device__ __forceinline__ void f32_join(const LinearArgs<float>& a, uint32_t sums, int rank, int m0,
+                                         int n0) {
+  constexpr int MINE = BM * BN / S / TH, BATCH = MINE < 32 / S ? MINE : 32 / S;
+  static_assert(BM % S == 0 && BM * BN % (S * TH) == 0 && MINE % BATCH == 0, "whole passes");
+#pragma unroll 1
+  for (int i0 = 0; i0 < MINE; i0 += BATCH) {
+    float part[BATCH][S];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int e = (i0 + i) * TH + static_cast<int>(threadIdx.x);
+      const uint32_t at = sums + static_cast<uint32_t>((e / BN * S + rank) * BN + e % BN) * 4u;
+#pragma unroll
+      for (int s = 0; s < S; ++s) part[i][s] = ld_shared_cluster_f32(cluster_addr(at, s));
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int e = (i0 + i) * TH + static_cast<int>(threadIdx.x);
+      const int m = m0 + e / BN * S + rank, n = n0 + e % BN;
+      float v = part[i][0];
+#pragma unroll
+      for (int s = 1; s < S; ++s) v += part[i][s];
+      if (m < a.M && n < a.N) linear_finish<ACT>(a, m, n, v);
+    }
+  }
+}
+
 template <int ACT, int BM, int BN, int TM, int TN, bool VEC>
 __global__ void __launch_bounds__(F32Tile<BM, BN, TM, TN>::THREADS)
     linear_f32_kernel(const LinearArgs<float> a, int m_tiles) {
@@ -225,19 +254,10 @@ __global__ void __launch_bounds__(F32Tile<BM, BN, TM, TN>::THREADS)
 #pragma unroll
       for (int j = 0; j < TN; ++j) smem[row_of(i) * BN + col_of(j)] = acc[i][j];
     cluster_sync_all();
-    const uint32_t base = smem_u32(smem);
-    for (int e = tid; e < BM * BN / splits; e += TH) {
-      const int r = e / BN * splits + rank, c = e % BN;
-      if (m0 + r >= a.M || n0 + c >= a.N) continue;
-      float part[8];
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-        part[s] = s < splits ? ld_shared_cluster_f32(cluster_addr(base + (r * BN + c) * 4u, s)) : 0.f;
-      float v = part[0];
-#pragma unroll
-      for (int s = 1; s < 8; ++s)
-        if (s < splits) v += part[s];
-      linear_finish<ACT>(a, m0 + r, n0 + c, v);
+    switch (splits) {
+      case 2: f32_join<ACT, BM, BN, TH, 2>(a, smem_u32(smem), rank, m0, n0); break;
+      case 4: f32_join<ACT, BM, BN, TH, 4>(a, smem_u32(smem), rank, m0, n0); break;
+      default: f32_join<ACT, BM, BN, TH, 8>(a, smem_u32(smem), rank, m0, n0); break;
     }
     cluster_sync_all();  // no CTA leaves while a peer may still read its sums
   }

@@ -378,11 +378,19 @@ struct ScanCut {
 
 ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   ScanCut c{};
-  c.short_call = p->T <= 32;
-  if (c.short_call) return c;
   c.per_group = int(cdiv(p->d / p->G, kScanCh));
   c.blocks = c.per_group * p->G;
   const long long groups = p->B * c.blocks, workers = (long long)kScanCtas * sms;
+  // Token after token, or chunks.  Measured at N = 4, 16, 64, B = 1, 8, 32 and d = 512
+  // to 5120 (us): the serial kernel takes 0.24 a token, or 1.4e-6 a state element and
+  // token where that is more; a wave of chunks 4 + 0.42 N, at least 7.5 in all.
+  // (B 8, d 5120, N 16: 60 and 116 at T = 64, 117 and 120 at 128, 229 and 138 at 256.
+  // B 1, d 512: 7.8 and 7.6 at T = 33.  B 32, d 1024, N 4: 57 and 97 at T = 256.)
+  const double elements = double(p->B) * p->d * p->T * double((p->N + 3) / 4 * 4);
+  const double serial_us = std::max(2.0 + 0.24 * p->T, 1.4e-6 * elements);
+  const double chunk_us = std::max(7.5, double(groups) * cdiv(p->T, kScanChunk) / workers * (4.0 + 0.42 * p->N));
+  c.short_call = p->T == 1 || serial_us < chunk_us;
+  if (c.short_call) return c;
   const long long chunks = cdiv(p->T, kScanChunk);
   long long run_chunks = chunks;
   if (groups * 4 >= workers * 3) {
@@ -391,9 +399,20 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
     c.chained = true;
     if (groups < 6 * workers) run_chunks = std::min(chunks, 4ll);
   } else {
-    // few channels: independent runs, two tasks for every CTA, a run of at least two chunks
-    const long long want = std::max(1ll, 2 * workers / groups);
-    run_chunks = std::min(chunks, std::max(2ll, cdiv(chunks, want)));
+    // few channels: one run, or independent runs whose two passes and join cost less.
+    // A chunk takes a CTA half a wave's time when it has the SM to itself, all of it
+    // when three share one; the state pass does 0.6 of the other's work.
+    const double wave = 4.0 + 0.42 * p->N;
+    auto chunk_time = [&](double tasks) { return wave * (0.5 + 0.5 * std::min(1.0, tasks / workers)); };
+    double best = double(chunks) * chunk_time(double(groups));
+    for (long long rc = 1; rc < chunks; rc *= 2) {
+      const long long tasks = groups * cdiv(chunks, rc);
+      const double cost = 1.6 * double(rc * cdiv(tasks, workers)) * chunk_time(double(tasks)) + 4.0;
+      if (cost < best) {
+        best = cost;
+        run_chunks = rc;
+      }
+    }
   }
   c.run_tokens = int(run_chunks * kScanChunk);
   c.runs = int(cdiv(chunks, run_chunks));
@@ -416,31 +435,32 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   return c;
 }
 
-template <typename T_>
-ittt_status scan_short(const ScanArgs<T_>& a, int sms, cudaStream_t st) {
+template <typename T_, bool VEC>
+ittt_status scan_short_sized(const ScanArgs<T_>& a, int sms, cudaStream_t st) {
   const int npl = a.N <= 128 ? 4 : 8;
   int lanes = 1;
   while (lanes * npl < a.N) lanes *= 2;
-  const int aligned = aligned16(a.A) && aligned16(a.state_in) && aligned16(a.state_out);
-  if (a.T == 1 && a.N <= 128) {
-    // four sequences a thread where that leaves 8 warps an SM, else one
-    constexpr uintptr_t quad = 4 * sizeof(T_) - 1;
-    const int vec_f32 = aligned && a.N % 4 == 0;
-    const int vec_bc = a.N % 4 == 0 && a.ldb % 4 == 0 && a.ldc % 4 == 0 &&
-                       ((reinterpret_cast<uintptr_t>(a.Bm) | reinterpret_cast<uintptr_t>(a.Cm)) & quad) == 0;
-    const long long threads = (long long)a.d * lanes;
-#ifndef TOKSEQ
-#define TOKSEQ 2
-#endif
-    if (TOKSEQ > 1 && cdiv(a.B, TOKSEQ) * threads >= 256ll * sms)
-      return launch_pdl(scan_token_kernel<T_, TOKSEQ>, dim3(unsigned(cdiv(cdiv(a.B, TOKSEQ) * threads, 128))),
-                        dim3(128), st, a, lanes, vec_f32, vec_bc);
-    return launch_pdl(scan_token_kernel<T_, 1>, dim3(unsigned(cdiv(a.B * threads, 128))), dim3(128), st,
-                      a, lanes, vec_f32, vec_bc);
+  const long long threads = (long long)a.d * lanes;
+  auto launch = [&](auto kern, long long batches) {
+    return launch_pdl(kern, dim3(unsigned(cdiv(batches * threads, 128))), dim3(128), st, a, lanes);
+  };
+  if (a.T == 1 && npl == 4) {
+    // two sequences a thread where that leaves every SM 8 warps, else one
+    if (cdiv(a.B, 2) * threads >= 256ll * sms) return launch(scan_token_kernel<T_, 2, VEC>,
+                                                               cdiv(a.B, 2));
+    return launch(scan_token_kernel<T_, 1, VEC>, a.B);
   }
-  const dim3 grid(unsigned(cdiv((long long)a.B * a.d * lanes, 128)));
-  if (npl == 4) return launch_pdl(scan_serial_kernel<T_, 4>, grid, dim3(128), st, a, lanes, aligned);
-  return launch_pdl(scan_serial_kernel<T_, 8>, grid, dim3(128), st, a, lanes, aligned);
+  if (npl == 4) return launch(scan_serial_kernel<T_, 4, VEC>, a.B);
+  return launch(scan_serial_kernel<T_, 8, VEC>, a.B);
+}
+
+template <typename T_>
+ittt_status scan_short(const ScanArgs<T_>& a, int sms, cudaStream_t st) {
+  constexpr uintptr_t quad = 4 * sizeof(T_) - 1;
+  const bool vec = a.N % 4 == 0 && a.ldb % 4 == 0 && a.ldc % 4 == 0 && aligned16(a.A) &&
+                   aligned16(a.state_in) && aligned16(a.state_out) &&
+                   ((reinterpret_cast<uintptr_t>(a.Bm) | reinterpret_cast<uintptr_t>(a.Cm)) & quad) == 0;
+  return vec ? scan_short_sized<T_, true>(a, sms, st) : scan_short_sized<T_, false>(a, sms, st);
 }
 
 template <typename T_, bool STATE_ONLY>

@@ -8,7 +8,7 @@
 //   scan_token_kernel   single tokens: lanes over the state, several sequences a
 //       thread.  Bound by the state's bytes.
 //   scan_serial_kernel  short calls: lanes over the state, four or eight elements a
-//       lane, token after token.
+//       lane, four tokens at a time.
 //   scan_chunk_kernel   prompts: 8 channels a CTA, 256 tokens at a time.  A
 //       thread owns two neighbouring channels and 8 consecutive tokens, a warp two
 //       channels and the whole chunk.  For four state elements at once a thread runs
@@ -80,10 +80,29 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 
 // ------------------------------------------------------------ short calls
 
-// NPL state elements a lane, `lanes` (a power of two) lanes a channel.
-template <typename T_, int NPL>
-__global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, int lanes,
-                                                          int aligned) {
+// Four neighbouring values as they are in memory.  The short kernels issue every
+// load before the first use of one, without branches between them: a conversion or a
+// condition after each load would wait for it.
+template <typename T_>
+struct alignas(4 * sizeof(T_)) Quad {
+  T_ v[4];
+  // VEC: one load of four values; else the first `live` >= 1 of them, the last repeated.
+  template <bool VEC>
+  __device__ __forceinline__ void load(const T_* p, int live) {
+    if (VEC) {
+      *this = *reinterpret_cast<const Quad*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = p[min(i, live - 1)];
+    }
+  }
+};
+
+// NPL state elements a lane, `lanes` (a power of two) lanes a channel, four tokens at
+// a time: the loads of the next four are under way while four are computed.
+template <typename T_, int NPL, bool VEC>
+__global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, int lanes) {
+  constexpr int Q = NPL / 4, TOK = 4;
   grid_dependency_wait();
   const long long gid = (blockIdx.x * 128ll + threadIdx.x) / lanes;
   const int sub = threadIdx.x & (lanes - 1);
@@ -92,106 +111,116 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, 
   const long long w = real ? gid : (long long)a.B * a.d - 1;
   const int b = static_cast<int>(w / a.d), c = static_cast<int>(w % a.d);
   const int g = c / (a.d / a.G);
-  const int n0 = sub * NPL;
-  const int live = min(NPL, a.N - n0);  // elements of this lane (may be <= 0)
   const int len = sequence_length(a.lengths, b, a.T);
-  const bool vec = aligned && live == NPL && (a.N & 3) == 0;
-  float h[NPL], A2[NPL];
+  int n0[Q], live[Q];  // first element and number of elements (may be <= 0) of each quad
+  float h[Q][4] = {}, A2[Q][4];
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) h[i] = A2[i] = 0.f;
-  if (vec) {
-    const float4* Ap = reinterpret_cast<const float4*>(a.A + (long long)c * a.N + n0);
-    const float4* hp =
-        a.state_in ? reinterpret_cast<const float4*>(a.state_in + w * a.N + n0) : nullptr;
+  for (int q = 0; q < Q; ++q) {
+    live[q] = a.N - (sub * NPL + 4 * q);
+    n0[q] = live[q] > 0 ? sub * NPL + 4 * q : 0;  // a quad past the end reads the first and drops it
+    Quad<float> v;
+    v.load<VEC>(a.A + (long long)c * a.N + n0[q], live[q] > 0 ? live[q] : a.N);
 #pragma unroll
-    for (int i = 0; i < NPL; i += 4) {
-      const float4 v = __ldg(Ap + i / 4);
-      A2[i] = v.x, A2[i + 1] = v.y, A2[i + 2] = v.z, A2[i + 3] = v.w;
-      if (hp) {
-        const float4 s = hp[i / 4];
-        h[i] = s.x, h[i + 1] = s.y, h[i + 2] = s.z, h[i + 3] = s.w;
-      }
+    for (int j = 0; j < 4; ++j) A2[q][j] = v.v[j] * kLog2e;
+    if (a.state_in) {
+      v.load<VEC>(a.state_in + w * a.N + n0[q], live[q] > 0 ? live[q] : a.N);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[q][j] = v.v[j];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (i < live) {
-        A2[i] = a.A[(long long)c * a.N + n0 + i];
-        if (a.state_in) h[i] = a.state_in[w * a.N + n0 + i];
-      }
   }
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) A2[i] *= kLog2e;
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
   const float skip = a.D ? a.D[c] : 0.f;
   const long long row0 = (long long)b * a.T;
   // the lanes of a warp may belong to sequences of different lengths
   const int warp_len = __reduce_max_sync(0xffffffffu, len);
-  for (int t = 0; t < warp_len; ++t) {
-    float y = 0.f, u = 0.f;
-    if (t < len) {
-      const long long row = row0 + t;
-      u = to_f32(a.U[row * a.ldu + c]);
-      float s = to_f32(a.delta[row * a.ldt + c]) + bias;
-      if (a.softplus) s = softplus_f32(s);
-      const float su = s * u;
-      const T_* Bp = a.Bm + row * a.ldb + (long long)g * a.N + n0;
-      const T_* Cp = a.Cm + row * a.ldc + (long long)g * a.N + n0;
+  if (warp_len > 0) {
+    T_ u[TOK], s[TOK], z[TOK];
+    Quad<T_> Bq[TOK][Q], Cq[TOK][Q];
+    const T_* zp = a.Z ? a.Z : a.U;  // a row of something where there is no gate
+    const long long ldz = a.Z ? a.ldz : a.ldu;
+    // tokens behind the end repeat the last one (an empty sequence its first row) and are dropped
+    auto load = [&](int t0) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (i < live) {
-          h[i] = fmaf(exp2_approx(s * A2[i]), h[i], su * to_f32(Bp[i]));
-          y = fmaf(h[i], to_f32(Cp[i]), y);
+      for (int i = 0; i < TOK; ++i) {
+        const long long row = row0 + max(min(t0 + i, len - 1), 0);
+        u[i] = a.U[row * a.ldu + c];
+        s[i] = a.delta[row * a.ldt + c];
+        z[i] = zp[row * ldz + c];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const long long at = (long long)g * a.N + n0[q];
+          Bq[i][q].template load<VEC>(a.Bm + row * a.ldb + at, live[q] > 0 ? live[q] : a.N);
+          Cq[i][q].template load<VEC>(a.Cm + row * a.ldc + at, live[q] > 0 ? live[q] : a.N);
         }
-    }
-    for (int o = lanes >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (t < len && sub == 0 && real) {
-      const long long row = row0 + t;
-      if (a.D) y = fmaf(skip, u, y);
-      if (a.Z) y *= silu_fast(to_f32(a.Z[row * a.ldz + c]));
-      a.Y[row * a.ldy + c] = from_f32<T_>(y);
+      }
+    };
+    load(0);
+    for (int t0 = 0; t0 < warp_len; t0 += TOK) {
+      float uf[TOK], sf[TOK], zf[TOK], Bf[TOK][Q][4], Cf[TOK][Q][4], y[TOK];
+#pragma unroll
+      for (int i = 0; i < TOK; ++i) {
+        uf[i] = to_f32(u[i]);
+        sf[i] = to_f32(s[i]) + bias;
+        zf[i] = to_f32(z[i]);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            Bf[i][q][j] = to_f32(Bq[i][q].v[j]);
+            Cf[i][q][j] = to_f32(Cq[i][q].v[j]);
+          }
+      }
+      load(t0 + TOK);
+#pragma unroll
+      for (int i = 0; i < TOK; ++i) {
+        const float st = a.softplus ? softplus_f32(sf[i]) : sf[i];
+        const float su = st * uf[i];
+        const bool in = t0 + i < len;
+        y[i] = 0.f;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float hn = fmaf(exp2_approx(st * A2[q][j]), h[q][j], su * Bf[i][q][j]);
+            if (in && j < live[q]) {
+              h[q][j] = hn;
+              y[i] = fmaf(hn, Cf[i][q][j], y[i]);
+            }
+          }
+      }
+      for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) y[i] += __shfl_xor_sync(0xffffffffu, y[i], o);
+#pragma unroll
+      for (int i = 0; i < TOK; ++i)
+        if (real && t0 + i < len && (i & (lanes - 1)) == sub) {
+          float v = y[i];
+          if (a.D) v = fmaf(skip, uf[i], v);
+          if (a.Z) v *= silu_fast(zf[i]);
+          a.Y[(row0 + t0 + i) * a.ldy + c] = from_f32<T_>(v);
+        }
     }
   }
   if (a.state_out && real) {
-    if (vec) {
-      float4* hp = reinterpret_cast<float4*>(a.state_out + w * a.N + n0);
 #pragma unroll
-      for (int i = 0; i < NPL; i += 4) hp[i / 4] = make_float4(h[i], h[i + 1], h[i + 2], h[i + 3]);
-    } else {
+    for (int q = 0; q < Q; ++q) {
+      float* p = a.state_out + w * a.N + n0[q];
+      if (VEC && live[q] > 0) {
+        *reinterpret_cast<float4*>(p) = make_float4(h[q][0], h[q][1], h[q][2], h[q][3]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (i < live) a.state_out[w * a.N + n0 + i] = h[i];
+        for (int j = 0; j < 4; ++j)
+          if (j < live[q]) p[j] = h[q][j];
+      }
     }
-  }
-}
-
-// Four values of a row.
-__device__ __forceinline__ void load_quad(const __nv_bfloat16* p, bool vec, int live, float (&v)[4]) {
-  if (vec) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
-    v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < live ? __bfloat162float(p[i]) : 0.f;
-  }
-}
-__device__ __forceinline__ void load_quad(const float* p, bool vec, int live, float (&v)[4]) {
-  if (vec) {
-    const float4 w = *reinterpret_cast<const float4*>(p);
-    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < live ? p[i] : 0.f;
   }
 }
 
 // Single tokens (N <= 128): four state elements a lane of one channel, for SEQ
 // sequences at once, so that A is read once for them and SEQ times as many bytes
 // of state are in flight.  Bound by reading and writing the state.
-template <typename T_, int SEQ>
-__global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs<T_> a, int lanes, int vec_f32,
-                                                         int vec_bc) {
+template <typename T_, int SEQ, bool VEC>
+__global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs<T_> a, int lanes) {
   grid_dependency_wait();
   const long long gid = (blockIdx.x * 128ll + threadIdx.x) / lanes;
   const int sub = threadIdx.x & (lanes - 1);
@@ -199,67 +228,63 @@ __global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs<T_> a, i
   // every thread of a warp stays for the shuffles; those past the end repeat the last channel
   const bool real = gid < (long long)batches * a.d;
   const long long w = real ? gid : (long long)batches * a.d - 1;
-  const int b0 = static_cast<int>(w / a.d) * SEQ, c = static_cast<int>(w % a.d);
+  const int b0 = static_cast<int>(w / a.d) * SEQ, c = static_cast<int>(w - (w / a.d) * a.d);
   const int g = c / (a.d / a.G);
-  const int n0 = sub * 4, live = min(4, a.N - n0);
-  const bool vf = vec_f32 && live == 4, vb = vec_bc && live == 4;
+  const int live = a.N - 4 * sub;                 // elements of this lane's quad (may be <= 0)
+  const int n0 = live > 0 ? 4 * sub : 0, some = live > 0 ? live : a.N;
   const long long cn = (long long)c * a.N + n0, gn = (long long)g * a.N + n0;
-  float A2[4] = {}, h[SEQ][4] = {}, bq[SEQ][4] = {}, cq[SEQ][4] = {}, u[SEQ], s[SEQ], z[SEQ];
-  // every load before any arithmetic (rows past the batch repeat the last one)
-  long long row[SEQ];
-#pragma unroll
-  for (int i = 0; i < SEQ; ++i) row[i] = min(b0 + i, a.B - 1);
-  if (live > 0) {
-#pragma unroll
-    for (int i = 0; i < SEQ; ++i)
-      if (a.state_in) load_quad(a.state_in + row[i] * a.d * a.N + cn, vf, live, h[i]);
-    load_quad(a.A + cn, vf, live, A2);
-#pragma unroll
-    for (int i = 0; i < SEQ; ++i) {
-      load_quad(a.Bm + row[i] * a.ldb + gn, vb, live, bq[i]);
-      load_quad(a.Cm + row[i] * a.ldc + gn, vb, live, cq[i]);
-    }
-  }
+  Quad<float> A, h[SEQ];
+  Quad<T_> Bq[SEQ], Cq[SEQ];
+  T_ u[SEQ], s[SEQ], z[SEQ];
+  int len[SEQ];
+  const T_* zp = a.Z ? a.Z : a.U;  // a row of something where there is no gate
+  const long long ldz = a.Z ? a.ldz : a.ldu;
+  const float* sp = a.state_in ? a.state_in : a.A;
+  const float from_state = a.state_in ? 1.f : 0.f;
 #pragma unroll
   for (int i = 0; i < SEQ; ++i) {
-    u[i] = to_f32(a.U[row[i] * a.ldu + c]);
-    s[i] = to_f32(a.delta[row[i] * a.ldt + c]);
-    z[i] = a.Z ? to_f32(a.Z[row[i] * a.ldz + c]) : 0.f;
+    const long long row = min(b0 + i, a.B - 1);  // past the batch: the last sequence again
+    h[i].template load<VEC>(sp + (a.state_in ? row * a.d * a.N + cn : cn), some);
+    Bq[i].template load<VEC>(a.Bm + row * a.ldb + gn, some);
+    Cq[i].template load<VEC>(a.Cm + row * a.ldc + gn, some);
+    u[i] = a.U[row * a.ldu + c];
+    s[i] = a.delta[row * a.ldt + c];
+    z[i] = zp[row * ldz + c];
+    len[i] = a.lengths ? a.lengths[row] : 1;
   }
+  A.load<VEC>(a.A + cn, some);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
   const float skip = a.D ? a.D[c] : 0.f;
 #pragma unroll
   for (int i = 0; i < SEQ; ++i) {
-    const bool in = real && b0 + i < a.B;
-    const bool on = in && (!a.lengths || a.lengths[row[i]] > 0);
+    const bool in = real && b0 + i < a.B, on = in && len[i] > 0;
+    const float uf = to_f32(u[i]);
+    float st = to_f32(s[i]) + bias;
+    if (a.softplus) st = softplus_f32(st);
+    const float su = st * uf;
     float y = 0.f;
-    if (on) {
-      float st = s[i] + bias;
-      if (a.softplus) st = softplus_f32(st);
-      const float su = st * u[i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float next = fmaf(exp2_approx(st * (A2[j] * kLog2e)), h[i][j], su * bq[i][j]);
-        if (j < live) {
-          h[i][j] = next;
-          y = fmaf(next, cq[i][j], y);
-        }
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float before = from_state != 0.f ? h[i].v[j] : 0.f;
+      const float next = fmaf(exp2_approx(st * (A.v[j] * kLog2e)), before, su * to_f32(Bq[i].v[j]));
+      if (j < live) y = fmaf(next, to_f32(Cq[i].v[j]), y);
+      h[i].v[j] = on ? next : before;  // an empty sequence passes its state through
     }
     for (int o = lanes >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    const long long row = b0 + i;
     if (on && sub == 0) {
-      if (a.D) y = fmaf(skip, u[i], y);
-      if (a.Z) y *= silu_fast(z[i]);
-      a.Y[row[i] * a.ldy + c] = from_f32<T_>(y);
+      if (a.D) y = fmaf(skip, uf, y);
+      if (a.Z) y *= silu_fast(to_f32(z[i]));
+      a.Y[row * a.ldy + c] = from_f32<T_>(y);
     }
-    if (a.state_out && in && live > 0) {  // an empty sequence passes its state through
-      float* p = a.state_out + row[i] * a.d * a.N + cn;
-      if (vf) {
-        *reinterpret_cast<float4*>(p) = make_float4(h[i][0], h[i][1], h[i][2], h[i][3]);
+    if (a.state_out && in) {
+      float* p = a.state_out + row * a.d * a.N + cn;
+      if (VEC && live > 0) {
+        *reinterpret_cast<Quad<float>*>(p) = h[i];
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (j < live) p[j] = h[i][j];
+          if (j < live) p[j] = h[i].v[j];
       }
     }
   }
