@@ -380,7 +380,8 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   ScanCut c{};
   c.per_group = int(cdiv(p->d / p->G, kScanCh));
   c.blocks = c.per_group * p->G;
-  const long long groups = p->B * c.blocks, workers = (long long)kScanCtas * sms;
+  const int ctas = p->dtype == ITTT_BF16 ? ScanShape<__nv_bfloat16>::CTAS : ScanShape<float>::CTAS;
+  const long long groups = p->B * c.blocks, workers = (long long)ctas * sms;
   // Token after token, or chunks.  Measured at N = 4, 16, 64, B = 1, 8, 32 and d = 512
   // to 5120 (us): the serial kernel takes 0.24 a token, or 1.4e-6 a state element and
   // token where that is more; a wave of chunks 4 + 0.42 N, at least 7.5 in all.
@@ -400,14 +401,15 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
     if (groups < 6 * workers) run_chunks = std::min(chunks, 4ll);
   } else {
     // few channels: one run, or independent runs whose two passes and join cost less.
-    // A chunk takes a CTA half a wave's time when it has the SM to itself, all of it
-    // when three share one; the state pass does 0.6 of the other's work.
+    // A chunk takes a CTA 0.6 of a wave's time when it has the SM to itself, all of it
+    // when the SM is full; the state pass does 0.6 of the other's work,
+    // and a task costs half a chunk more than its chunks.
     const double wave = 4.0 + 0.42 * p->N;
-    auto chunk_time = [&](double tasks) { return wave * (0.5 + 0.5 * std::min(1.0, tasks / workers)); };
+    auto chunk_time = [&](double tasks) { return wave * (0.6 + 0.4 * std::min(1.0, tasks / workers)); };
     double best = double(chunks) * chunk_time(double(groups));
-    for (long long rc = 1; rc < chunks; rc *= 2) {
+    for (long long rc = 1; rc < chunks; rc += std::max(1ll, rc / 8)) {
       const long long tasks = groups * cdiv(chunks, rc);
-      const double cost = 1.6 * double(rc * cdiv(tasks, workers)) * chunk_time(double(tasks)) + 4.0;
+      const double cost = 1.6 * (double(rc) + 0.5) * double(cdiv(tasks, workers)) * chunk_time(double(tasks)) + 4.0;
       if (cost < best) {
         best = cost;
         run_chunks = rc;
@@ -469,7 +471,7 @@ ittt_status scan_chunks(const ScanArgs<T_>& a, const ScanPlan& pl, long long tas
   static std::atomic<bool> granted[kMaxDevices] = {};
   auto kern = scan_chunk_kernel<T_, STATE_ONLY>;
   if (!grant_smem(kern, scan_smem_bytes<T_>(256), granted)) return ITTT_ERR_CUDA;
-  return launch_clusters(kern, unsigned(std::min<long long>(tasks, (long long)kScanCtas * sms)), 1, kScanThreads,
+  return launch_clusters(kern, unsigned(std::min<long long>(tasks, (long long)ScanShape<T_>::CTAS * sms)), 1, kScanThreads,
                          scan_smem_bytes<T_>(a.N), st, a, pl, g_wait_ns.load());
 }
 

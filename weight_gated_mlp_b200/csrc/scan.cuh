@@ -292,13 +292,14 @@ __global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs<T_> a, i
 
 // ---------------------------------------------------------------- prompts
 
-// Four warps and 168 registers a thread, three CTAs an SM, two pairs at once:
-// 470 us for 8192 x 5120 x 16 in bf16; one pair at once 491 us, with 128 registers
-// and four CTAs 534 us (584 us with two pairs, which then spill), eight warps and
-// 128 registers 514 us, 255 registers and two CTAs 532 us.
+// Four warps, two pairs at once, and in bf16 168 registers a thread and three CTAs an
+// SM: 470 us for 8192 x 5120 x 16.  One pair at once 491 us, with 128 registers and
+// four CTAs 534 us (584 us with two pairs, which then spill), eight warps and 128
+// registers 514 us, 255 registers and two CTAs 532 us, spans of four tokens 517 us.
+// fp32 holds twice the values of B and C and wants the registers: 80 us with two CTAs
+// for 1667 tokens x 1000 x 32, 105 us with three.
 constexpr int kScanWarps = 4;
 constexpr int kScanThreads = 32 * kScanWarps;
-constexpr int kScanCtas = 3;              // CTAs an SM
 constexpr int kScanCh = 2 * kScanWarps;           // channels a CTA, two a warp
 constexpr int kScanK = 8;                         // tokens a span, one span a lane
 constexpr int kScanChunk = 32 * kScanK;           // tokens a chunk
@@ -327,6 +328,7 @@ template <typename T_>
 struct ScanShape {
   static constexpr int ES = int(sizeof(T_));
   static constexpr int SLAB = 32 / ES;                       // state elements
+  static constexpr int CTAS = ES == 2 ? 3 : 2;               // CTAs an SM
   static constexpr int PAIRS = SLAB / 2;
   static constexpr int ROW_SPAN = kScanK * kScanCh + 16 / ES;  // elements between spans of raw rows
   static constexpr int ROW_TILE = 32 * ROW_SPAN;
@@ -504,7 +506,7 @@ __device__ __forceinline__ void store_two(float* p, float x, float y) {
 // STATE_ONLY: the first of the two passes of a call that is split over time: every
 // run from a zero state, its end state and sum of steps written, no outputs.
 template <typename T_, bool STATE_ONLY>
-__global__ void __launch_bounds__(kScanThreads, kScanCtas)
+__global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
     scan_chunk_kernel(const ScanArgs<T_> a, const ScanPlan pl, unsigned long long wait_ns) {
   using S = ScanShape<T_>;
   extern __shared__ __align__(16) uint8_t scan_smem[];

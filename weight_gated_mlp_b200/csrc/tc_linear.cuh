@@ -198,7 +198,10 @@ __global__ void __launch_bounds__(192, SplitShape<MT>::CTAS)
     }
     __syncwarp();
   }
-  // the next kernel's prologue may start; it waits for this grid before it reads
+  // The next kernel's CTAs may take free slots and set up (every CTA of this one holds
+  // its TMEM): 11.9 us a call instead of 13.7 for one row of 9728 -> 2560 in a chain of
+  // calls.  Before the wait above it is 12.4, and in the other kernels of these
+  // operators, which leave no slot unused, it costs time.
   grid_launch_dependents();
 
   // every MMA has completed, and with them every read of the pipeline's memory
