@@ -178,10 +178,9 @@ int resident_pairs(int sms) {
 
 // Persistent CTA pairs.
 template <int ACT>
-ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int mt, int pairs, cudaStream_t st) {
+ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int pairs, cudaStream_t st) {
   PairTile t{};
-  t.mt = mt;
-  t.m_tiles = int(cdiv(a.M, mt));
+  t.m_tiles = int(cdiv(a.M, kPairRows));
   t.n_tiles = int(cdiv(a.N, 256));
   t.num_kb = int(cdiv(a.K, 64));
   // a group's rows of W (about 32 MiB) stay in L2 while the rows of X pass once
@@ -189,7 +188,7 @@ ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int mt, int pairs, 
   if (tile_bytes * t.n_tiles > (48ll << 20)) t.group_n = int(std::max(1ll, (32ll << 20) / tile_bytes));
   if ((long long)t.m_tiles * t.n_tiles >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
   CUtensorMap w, x;
-  if (!make_map(&w, a.W, a.K, a.N, a.K, 64, 128) || !make_map(&x, a.X, a.K, a.M, a.ldx, 64, mt / 2))
+  if (!make_map(&w, a.W, a.K, a.N, a.K, 64, 128) || !make_map(&x, a.X, a.K, a.M, a.ldx, 64, kPairRows / 2))
     return ITTT_ERR_CUDA;
   const long long units = (long long)t.m_tiles * t.n_tiles;
   return launch_clusters(linear_pair_kernel<ACT>, unsigned(2 * std::min<long long>(units, pairs)), 2, 192,
@@ -197,10 +196,10 @@ ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int mt, int pairs, 
 }
 
 // Up to 128 rows: one narrow tile of all rows per 128 outputs, so that W is read
-// once.  More: pairs when 256 x 256 tiles fill at least three quarters of the
-// SMs, with the tile height (256, 224, ... 128 rows) whose waves of tiles cost
-// least; else 128 x 128 tiles, or 128 x 64 where even eight-fold splits of those
-// leave SMs empty.
+// once.  More: split tiles of 128 x 128 while K can still be split over two CTAs (the
+// pairs' 256 x 256 tiles leave most SMs empty there: 512 x 9728 x 2560 takes 48 us
+// split and 61 in pairs), of 128 x 64 where even eight-fold splits of those leave SMs
+// empty; from there on pairs (1024 x 9728 x 2560: 61 us, 80 us in unsplit tiles).
 template <int ACT>
 ittt_status linear_bf16(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
   const int sms = num_sms();
@@ -211,10 +210,7 @@ ittt_status linear_bf16(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
   if (a.M <= 128) return linear_split<128, ACT>(a, sms, st);
   const int pairs = resident_pairs<ACT>(sms);
   if (pairs <= 0) return ITTT_ERR_CUDA;
-  const long long n_tiles = cdiv(a.N, 256);
-  if (n_tiles * cdiv(a.M, 256) * 4 >= pairs * 3) {
-    return linear_pairs<ACT>(a, 256, pairs, st);
-  }
+  if (cdiv(a.N, 128) * cdiv(a.M, 128) > sms) return linear_pairs<ACT>(a, pairs, st);
   if (cdiv(a.N, 128) * cdiv(a.M, 128) * 8 < sms) return linear_split<64, ACT>(a, sms, st);
   return linear_split<128, ACT>(a, sms, st);
 }

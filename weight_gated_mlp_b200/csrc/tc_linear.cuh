@@ -12,8 +12,7 @@
 //       tile and split K, their sums joined through distributed shared memory in
 //       rank order (the same bits every time, no workspace, one launch).  For few
 //       rows it is bound by reading W once from HBM.
-//   linear_pair_kernel   persistent CTA pairs (two SMs, one 256-lane tile, MT up to
-//       256 columns, two TMEM slots so that a tile's epilogue overlaps the next
+//   linear_pair_kernel   persistent CTA pairs (two SMs, one 256-lane tile, 256 columns, two TMEM slots so that a tile's epilogue overlaps the next
 //       tile's main loop).  For many rows: bound by the tensor cores.
 #pragma once
 
@@ -267,13 +266,13 @@ __global__ void __launch_bounds__(192, SplitShape<MT>::CTAS)
 // ------------------------------------------------------------------ pairs
 
 struct PairTile {
-  int mt;                     // rows of X per tile, a multiple of 16, at most 256
-  int m_tiles, n_tiles;       // n_tiles: 256 outputs each
+  int m_tiles, n_tiles;       // tiles of 256 rows of X and of 256 outputs
   int group_n;                // n-tiles per rasterisation group (0 = all): their rows of W
                               // stay in L2 while the rows of X pass
   int num_kb;
 };
 
+constexpr int kPairRows = 256;  // rows of X a tile: 128 and 224 take as long per step of K (0.4 us)
 constexpr int kPairStages = 6;
 constexpr int kPairStageBytes = 2 * 128 * 128;
 constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024 + 256;
@@ -308,8 +307,7 @@ __global__ void __launch_bounds__(192, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_cta_rank();
   const bool leader = rank == 0;
-  const int half = t.mt >> 1;  // rows of X each CTA of the pair loads
-  const uint32_t x_bytes = static_cast<uint32_t>(half) * 128u;
+  constexpr int half = kPairRows / 2;  // rows of X each CTA of the pair loads
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
@@ -352,10 +350,10 @@ __global__ void __launch_bounds__(192, 1)
         int mt, nt;
         pair_decode(t, u, mt, nt);
         const int n0 = nt * 256 + static_cast<int>(rank) * 128;
-        const int m0 = mt * t.mt + static_cast<int>(rank) * half;
+        const int m0 = mt * kPairRows + static_cast<int>(rank) * half;
         for (int kb = 0; kb < t.num_kb; ++kb) {
           if (!(ok = mbar_wait(&empty_bar[stage], phase ^ 1, wc))) break;
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2u * (128u * 128u + x_bytes));
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2u * kPairStageBytes);
           last_parity[stage] = static_cast<int>(phase);
           uint8_t* sa = smem + stage * kPairStageBytes;
           const uint32_t fb = leader_bar(&full_bar[stage]);
@@ -374,8 +372,8 @@ __global__ void __launch_bounds__(192, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
-      // 256 lanes x mt columns over the two SMs
-      const uint32_t idesc = make_idesc_bf16(256, t.mt, false, false);
+      // 256 lanes x 256 columns over the two SMs
+      constexpr uint32_t idesc = make_idesc_bf16(256, kPairRows, false, false);
       int stage = 0;
       uint32_t phase = 0;
       uint32_t count[2] = {0, 0};
@@ -427,11 +425,11 @@ __global__ void __launch_bounds__(192, 1)
       int mt, nt;
       pair_decode(t, u, mt, nt);
       const int n = nt * 256 + static_cast<int>(rank) * 128 + r;
-      const int m0 = mt * t.mt;
+      const int m0 = mt * kPairRows;
       const float bias = (a.bias && n < a.N) ? __bfloat162float(a.bias[n]) : 0.f;
       // this warp's 64 bytes of the tile's residual rows come into L2 during the main loop
       if (a.residual && n - lane < a.N)
-        for (int i = lane; i < t.mt && m0 + i < a.M; i += 32)
+        for (int i = lane; i < kPairRows && m0 + i < a.M; i += 32)
           prefetch_l2(a.residual + (long long)(m0 + i) * a.ldr + n - lane);
       const bool ok = mbar_wait(&tfull[slot], count[slot] & 1, wc);
       __syncwarp();
@@ -440,13 +438,13 @@ __global__ void __launch_bounds__(192, 1)
       tc_fence_after_sync();
       const uint32_t tbase = tmem_base + lane_addr + static_cast<uint32_t>(slot) * 256u;
 #pragma unroll 1
-      for (int c0 = 0; c0 < t.mt; c0 += 32) {
+      for (int c0 = 0; c0 < kPairRows; c0 += 32) {
         uint32_t v[32];
         __syncwarp();
-        tmem_ld32(tbase + c0, v);  // past t.mt: columns of the slot that no row belongs to
+        tmem_ld32(tbase + c0, v);
         tmem_ld_wait();
-        if (c0 + 32 >= t.mt) release(slot);
-        linear_store32<ACT>(a, v, n, m0 + c0, min(t.mt - c0, a.M - (m0 + c0)), bias);
+        if (c0 + 32 == kPairRows) release(slot);
+        linear_store32<ACT>(a, v, n, m0 + c0, min(kPairRows - c0, a.M - (m0 + c0)), bias);
       }
       slot ^= 1;
     }
