@@ -427,7 +427,7 @@ typedef struct {
 /* Y = act(X W^T + bias) + residual.
  * X [M, K]; W [N, K] (nn.Linear layout); bias [N] or NULL; residual [M, N] or
  * NULL, may be Y itself (with ldr = ldy) and must not overlap Y otherwise;
- * Y [M, N].  Sums are held in fp32 and the epilogue computes in fp32 with one
+ * Y [M, N], which must not overlap X, W or bias.  Sums are held in fp32 and the epilogue computes in fp32 with one
  * rounding on the store.  bf16: K % 8 == 0, ldx % 8 == 0, X and W 16-byte
  * aligned (else ITTT_ERR_UNSUPPORTED); M, N, ldr and ldy are free.  f32: any
  * sizes.  The result does not depend on what ran before or beside the call. */

@@ -28,6 +28,7 @@ def _linear(**kw):
     (dict(M=0), INV), (dict(N=-1), INV), (dict(K=0), INV), (dict(dtype=2), INV), (dict(act=5), INV),
     (dict(act=-1), INV), (dict(ldx=8), INV), (dict(ldr=23), INV), (dict(ldy=1), INV),
     (dict(ldx=-16), INV), (dict(K=12), UNS), (dict(ldx=20), UNS), (dict(M=1 << 31), UNS),
+    (dict(M=(1 << 31) - 512), UNS), (dict(N=(1 << 31) - 8), UNS),
 ])
 def test_linear_problems(lib, kw, status):
     p = _linear(**kw)
@@ -41,8 +42,12 @@ def test_linear_pointers(lib):
     assert lib.ittt_linear(r, None, FAKE, None, None, FAKE, None) == INV
     assert lib.ittt_linear(r, FAKE, None, None, None, FAKE, None) == INV
     assert lib.ittt_linear(r, FAKE, FAKE, None, None, None, None) == INV
-    assert lib.ittt_linear(r, odd, FAKE, None, None, FAKE, None) == UNS
-    assert lib.ittt_linear(r, FAKE, odd, None, None, FAKE, None) == UNS
+    y = ctypes.c_void_p(1 << 23)
+    assert lib.ittt_linear(r, odd, FAKE, None, None, y, None) == UNS
+    assert lib.ittt_linear(r, FAKE, odd, None, None, y, None) == UNS
+    # Y may be the residual, not an operand of the product
+    assert lib.ittt_linear(r, FAKE, ctypes.c_void_p(1 << 22), None, None, FAKE, None) == INV
+    assert lib.ittt_linear(r, ctypes.c_void_p(1 << 22), FAKE, None, None, FAKE, None) == INV
     # in place only with one row stride
     q = _linear(ldr=32)
     assert lib.ittt_linear(ctypes.byref(q), FAKE, FAKE, None, FAKE, FAKE, None) == INV
@@ -58,7 +63,8 @@ def _conv(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(B=0), INV), (dict(T=0), INV), (dict(d=-1), INV), (dict(k=0), INV), (dict(k=17), UNS),
     (dict(dtype=9), INV), (dict(act=9), INV), (dict(reserved=1), INV), (dict(ldx=15), INV),
-    (dict(ldy=2), INV), (dict(T=1 << 31), UNS), (dict(d=1 << 31), UNS),
+    (dict(ldy=2), INV), (dict(T=1 << 31), UNS), (dict(d=1 << 31), UNS), (dict(B=1 << 16), UNS),
+    (dict(B=4, T=1 << 29), UNS),
 ])
 def test_conv_problems(lib, kw, status):
     p = _conv(**kw)
@@ -73,6 +79,8 @@ def test_conv_pointers(lib):
     assert lib.ittt_causal_conv(r, FAKE, None, None, None, None, other, None, None) == INV
     assert lib.ittt_causal_conv(r, FAKE, FAKE, None, None, None, None, None, None) == INV
     assert lib.ittt_causal_conv(r, FAKE, FAKE, None, None, None, FAKE, None, None) == INV  # Y = X
+    assert lib.ittt_causal_conv(r, FAKE, FAKE, None, other, None, other, None, None) == INV
+    assert lib.ittt_causal_conv(r, FAKE, FAKE, None, None, None, other, other, None) == INV
 
 
 def _scan(**kw):

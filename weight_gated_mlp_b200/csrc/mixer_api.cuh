@@ -18,10 +18,10 @@ size_t span_bytes(long long rows, long long ld, long long width, size_t es) {
   return (size_t(rows - 1) * size_t(ld) + size_t(width)) * es;
 }
 
-// Row counts and widths fit 32 bits, a whole matrix fits 2^62 bytes.
+// Row and column numbers, rounded up to a tile, fit 32 bits; offsets are 64-bit.
 bool fits(int64_t rows, int64_t width, int64_t ld) {
-  constexpr int64_t k31 = 1ll << 31;
-  return rows > 0 && width > 0 && rows < k31 && width < k31 && (ld == 0 || (ld >= width && ld < k31));
+  constexpr int64_t most = (1ll << 31) - 1024;
+  return rows > 0 && width > 0 && rows < most && width < most && (ld == 0 || (ld >= width && ld < most));
 }
 
 // ------------------------------------------------------------------ linear
@@ -32,7 +32,8 @@ ittt_status validate_linear(const ittt_linear_problem* p) {
     return ITTT_ERR_INVALID_ARG;
   if ((p->ldx && p->ldx < p->K) || (p->ldr && p->ldr < p->N) || (p->ldy && p->ldy < p->N))
     return ITTT_ERR_INVALID_ARG;
-  if (!fits(p->M, p->K, p->ldx) || !fits(p->M, p->N, p->ldr) || !fits(p->M, p->N, p->ldy))
+  if (!fits(p->M, p->K, p->ldx) || !fits(p->M, p->N, p->ldr) || !fits(p->M, p->N, p->ldy) ||
+      !fits(p->N, p->K, 0))
     return ITTT_ERR_UNSUPPORTED;
   if (p->dtype == ITTT_BF16 && (p->K % 8 || p->ldx % 8)) return ITTT_ERR_UNSUPPORTED;
   return ITTT_OK;
@@ -238,7 +239,7 @@ ittt_status validate_conv(const ittt_conv_problem* p) {
       p->reserved != 0 || !valid_dtype_act(p->dtype, p->act))
     return ITTT_ERR_INVALID_ARG;
   if ((p->ldx && p->ldx < p->d) || (p->ldy && p->ldy < p->d)) return ITTT_ERR_INVALID_ARG;
-  if (p->k > 16 || p->B > 65535 || p->T >= (1ll << 31) || p->B * p->T >= (1ll << 31) ||
+  if (p->k > 16 || p->B > 65535 || p->T > (1ll << 30) ||
       !fits(p->B * p->T, p->d, p->ldx) || !fits(p->B * p->T, p->d, p->ldy))
     return ITTT_ERR_UNSUPPORTED;
   return ITTT_OK;
@@ -323,8 +324,7 @@ ittt_status validate_scan(const ittt_scan_problem* p) {
   for (int i = 0; i < 6; ++i)
     if (ld[i] < 0 || (ld[i] && ld[i] < (i < 4 ? p->d : gn))) return ITTT_ERR_INVALID_ARG;
   if (p->d % p->G != 0) return ITTT_ERR_INVALID_ARG;
-  if (p->N > 256 || p->B >= (1ll << 31) || p->T >= (1ll << 31) || p->B * p->T >= (1ll << 31))
-    return ITTT_ERR_UNSUPPORTED;
+  if (p->N > 256 || p->B >= (1ll << 31) || p->T > (1ll << 30)) return ITTT_ERR_UNSUPPORTED;
   for (int i = 0; i < 6; ++i)
     if (!fits(p->B * p->T, i < 4 ? p->d : gn, ld[i])) return ITTT_ERR_UNSUPPORTED;
   if (p->B * p->d >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
@@ -515,7 +515,7 @@ ittt_status ittt_linear(const ittt_linear_problem* p, const void* X, const void*
   const NvtxRange nvtx_range("ittt_linear");
   ittt_status s = validate_linear(p);
   if (s != ITTT_OK) return s;
-  if (!X || !W || !Y) return ITTT_ERR_INVALID_ARG;
+  if (!X || !W || !Y || Y == X || Y == W || Y == bias) return ITTT_ERR_INVALID_ARG;
   if (residual == Y && stride_or(p->ldr, p->N) != stride_or(p->ldy, p->N)) return ITTT_ERR_INVALID_ARG;
   const size_t es = p->dtype == ITTT_BF16 ? 2 : 4;
   if ((s = check_buffers({{X, span_bytes(p->M, stride_or(p->ldx, p->K), p->K, es)},
@@ -537,7 +537,7 @@ ittt_status ittt_causal_conv(const ittt_conv_problem* p, const void* X, const vo
   const NvtxRange nvtx_range("ittt_causal_conv");
   ittt_status s = validate_conv(p);
   if (s != ITTT_OK) return s;
-  if (!X || !conv_kernel || !Y || X == Y) return ITTT_ERR_INVALID_ARG;
+  if (!X || !conv_kernel || !Y || X == Y || Y == state_in || Y == state_out) return ITTT_ERR_INVALID_ARG;
   const size_t es = p->dtype == ITTT_BF16 ? 2 : 4;
   const long long rows = p->B * p->T;
   const size_t state = size_t(p->B) * size_t(p->k - 1) * p->d * es;
@@ -575,7 +575,8 @@ ittt_status ittt_selective_scan(const ittt_scan_problem* p, const void* U, const
   ittt_status s = validate_scan(p);
   if (s != ITTT_OK) return s;
   if (!U || !delta || !A || !Bm || !Cm || !Y) return ITTT_ERR_INVALID_ARG;
-  if (Y == U || Y == delta || Y == Z || Y == Bm || Y == Cm) return ITTT_ERR_INVALID_ARG;
+  if (Y == U || Y == delta || Y == Z || Y == Bm || Y == Cm || Y == state_in || Y == state_out)
+    return ITTT_ERR_INVALID_ARG;
   const size_t es = p->dtype == ITTT_BF16 ? 2 : 4;
   const long long rows = p->B * p->T, gn = (long long)p->G * p->N;
   const size_t state = size_t(p->B) * p->d * p->N * 4;

@@ -561,11 +561,11 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
     const bool first = run == 0;
     const bool last = len <= t_begin + pl.run_tokens;  // the run that holds the sequence's end
     if (!first && t_begin >= len) {
-      if (!STATE_ONLY) continue;
-      // a run behind the end joins as nothing
-      for (int e = tid; e < nch * a.N; e += kScanThreads)
-        pl.carry[((long long)run * a.B + b) * a.d * a.N + (long long)c0 * a.N + e] = 0.f;
-      if (tid < nch) pl.step_sum[((long long)run * a.B + b) * a.d + c0 + tid] = 0.f;
+      if constexpr (STATE_ONLY) {  // a run behind the end joins as nothing
+        const long long at = ((long long)run * a.B + b) * a.d + c0;
+        for (int e = tid; e < nch * a.N; e += kScanThreads) pl.carry[at * a.N + e] = 0.f;
+        if (tid < nch) pl.step_sum[at + tid] = 0.f;
+      }
       continue;
     }
 
