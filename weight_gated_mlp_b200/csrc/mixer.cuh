@@ -102,7 +102,7 @@ __device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, in
 // (nobody else does: the others start at token 8 or later) before it writes the same
 // channels' state_out, so the two may be one buffer.
 template <typename T_, int V, int KT, int ACT>
-__global__ void __launch_bounds__(128) causal_conv_vec_kernel(const CausalConvArgs<T_> a,
+__global__ void __launch_bounds__(128, V > 1 && KT <= 4 ? 4 : 1) causal_conv_vec_kernel(const CausalConvArgs<T_> a,
                                                               unsigned total, unsigned groups,
                                                               unsigned runs, int steps) {
   using Row = std::conditional_t<V == 1, T_, uint4>;

@@ -245,16 +245,13 @@ ittt_status validate_conv(const ittt_conv_problem* p) {
   return ITTT_OK;
 }
 
-#ifndef CONV_STEPS
-#define CONV_STEPS 8
-#endif
 // Steps of four tokens a thread: 8 while that leaves every SM 16 warps, down to 2.
 template <typename T_, int V, int KT, int ACT>
 ittt_status causal_conv_vec(const CausalConvArgs<T_>& a, cudaStream_t st) {
   const int sms = num_sms();
   if (sms <= 0) return ITTT_ERR_CUDA;
   const long long groups = a.d / V;
-  int steps = CONV_STEPS;
+  int steps = 8;
   while (steps > 2 && a.B * cdiv(a.T, 4 * steps) * groups < 512ll * sms) steps /= 2;
   const long long runs = cdiv(a.T, 4 * steps), total = a.B * runs * groups;
   if (total >= (1ll << 32) - 128) return ITTT_ERR_UNSUPPORTED;
@@ -368,49 +365,58 @@ ScanArgs<T_> scan_args(const ittt_scan_problem* p, const void* U, const void* de
 // How a call is cut (see ScanPlan).  short_call: the serial kernel.
 struct ScanCut {
   bool short_call, chained;
+  int passes;                            // the chunk kernel's P
   int runs, run_tokens, blocks, per_group;
   size_t flags, carry, step_sum, total;  // workspace offsets and size
 };
 
 ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   ScanCut c{};
-  c.per_group = int(cdiv(p->d / p->G, kScanCh));
+  const int ctas = p->dtype == ITTT_BF16 ? ScanShape<__nv_bfloat16, 1>::CTAS : ScanShape<float, 1>::CTAS;
+  const long long workers = (long long)ctas * sms;
+  // the wider channel blocks where they still fill the GPU (few, long sequences: as
+  // independent runs), the narrow ones else; a state of more than one slab of B and C
+  // would be staged once a pass and gain nothing
+  const long long wide = p->B * p->G * cdiv(p->d / p->G, scan_ch(2));
+  const bool few = wide * 4 < workers && cdiv(p->T, kScanChunk) * wide >= 4 * workers;
+  c.passes = p->dtype == ITTT_BF16 && p->N <= 16 && (wide >= workers || few) ? 2 : 1;
+  c.per_group = int(cdiv(p->d / p->G, scan_ch(c.passes)));
   c.blocks = c.per_group * p->G;
-  const int ctas = p->dtype == ITTT_BF16 ? ScanShape<__nv_bfloat16>::CTAS : ScanShape<float>::CTAS;
-  const long long groups = p->B * c.blocks, workers = (long long)ctas * sms;
+  const long long groups = p->B * c.blocks;
   // Token after token, or chunks.  Measured at N = 4, 16, 64, B = 1, 8, 32 and d = 512
   // to 5120 (us): the serial kernel takes 0.24 a token, or 1.4e-6 a state element and
   // token where that is more; a wave of chunks 4 + 0.42 N, at least 7.5 in all.
-  // (B 8, d 5120, N 16: 60 and 116 at T = 64, 117 and 120 at 128, 229 and 138 at 256.
+  // (B 8, d 5120, N 16: 60 and 116 at T = 64, 117 and 120 at 128, 229 and 138 at 256;
   // B 1, d 512: 7.8 and 7.6 at T = 33.  B 32, d 1024, N 4: 57 and 97 at T = 256.)
   const double elements = double(p->B) * p->d * p->T * double((p->N + 3) / 4 * 4);
   const double serial_us = std::max(2.0 + 0.24 * p->T, 1.4e-6 * elements);
-  const double chunk_us = std::max(7.5, double(groups) * cdiv(p->T, kScanChunk) / workers * (4.0 + 0.42 * p->N));
+  const double wave = c.passes == 2 ? 11.7 + 0.45 * p->N : 4.0 + 0.42 * p->N;
+  const double chunk_us = std::max(c.passes == 2 ? 13.0 : 7.5, double(groups) * cdiv(p->T, kScanChunk) / workers * wave);
   c.short_call = p->T == 1 || serial_us < chunk_us;
   if (c.short_call) return c;
   const long long chunks = cdiv(p->T, kScanChunk);
   long long run_chunks = chunks;
-  if (groups * 4 >= workers * 3) {
-    // enough channel blocks for every CTA: runs of 4 chunks, chained, so that the
-    // work is dealt out evenly however many blocks there are
-    c.chained = true;
-    if (groups < 6 * workers) run_chunks = std::min(chunks, 4ll);
-  } else {
-    // few channels: one run, or independent runs whose two passes and join cost less.
-    // A chunk takes a CTA 0.6 of a wave's time when it has the SM to itself, all of it
-    // when the SM is full; the state pass does 0.6 of the other's work,
-    // and a task costs half a chunk more than its chunks.
-    const double wave = 4.0 + 0.42 * p->N;
-    auto chunk_time = [&](double tasks) { return wave * (0.6 + 0.4 * std::min(1.0, tasks / workers)); };
-    double best = double(chunks) * chunk_time(double(groups));
-    for (long long rc = 1; rc < chunks; rc += std::max(1ll, rc / 8)) {
-      const long long tasks = groups * cdiv(chunks, rc);
-      const double cost = 1.6 * (double(rc) + 0.5) * double(cdiv(tasks, workers)) * chunk_time(double(tasks)) + 4.0;
-      if (cost < best) {
-        best = cost;
-        run_chunks = rc;
-      }
+  // One pass over whole sequences, or independent runs whose two passes and join cost
+  // less.  A chunk takes a CTA 0.6 of a wave's time when it has the SM to itself, all of
+  // it when the SM is full; the state pass does 0.6 of the other's work, and a task
+  // costs half a chunk more than its chunks.
+  auto chunk_time = [&](double tasks) { return wave * (0.6 + 0.4 * std::min(1.0, tasks / workers)); };
+  double best = double(chunks) * chunk_time(double(groups)) * std::max(1.0, double(groups) / workers);
+  bool split = false;
+  for (long long rc = 1; rc < chunks; rc += std::max(1ll, rc / 8)) {
+    const long long tasks = groups * cdiv(chunks, rc);
+    const double cost = 1.6 * (double(rc) + 0.5) * double(cdiv(tasks, workers)) * chunk_time(double(tasks)) + 4.0;
+    if (cost < best) {
+      best = cost;
+      run_chunks = rc;
+      split = true;
     }
+  }
+  if (!split && groups >= sms && groups < 6 * workers) {
+    // runs of four chunks, chained, so that the work is dealt out evenly however many
+    // channel blocks there are
+    c.chained = true;
+    run_chunks = std::min(chunks, 4ll);
   }
   c.run_tokens = int(run_chunks * kScanChunk);
   c.runs = int(cdiv(chunks, run_chunks));
@@ -424,7 +430,7 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   };
   if (c.chained) {
     c.flags = take(size_t(1 + groups) * 4);
-    c.carry = take(size_t(groups) * kScanCh * np * 4);
+    c.carry = take(size_t(groups) * scan_ch(c.passes) * np * 4);
   } else {
     c.carry = take(size_t(c.runs - 1) * p->B * p->d * p->N * 4);
     c.step_sum = take(size_t(c.runs - 1) * p->B * p->d * 4);
@@ -461,14 +467,23 @@ ittt_status scan_short(const ScanArgs<T_>& a, int sms, cudaStream_t st) {
   return vec ? scan_short_sized<T_, true>(a, sms, st) : scan_short_sized<T_, false>(a, sms, st);
 }
 
-template <typename T_, bool STATE_ONLY>
-ittt_status scan_chunks(const ScanArgs<T_>& a, const ScanPlan& pl, long long tasks, int sms,
+template <typename T_, int P, bool STATE_ONLY>
+ittt_status scan_chunks_wide(const ScanArgs<T_>& a, const ScanPlan& pl, long long tasks, int sms,
                         cudaStream_t st) {
   static std::atomic<bool> granted[kMaxDevices] = {};
-  auto kern = scan_chunk_kernel<T_, STATE_ONLY>;
-  if (!grant_smem(kern, scan_smem_bytes<T_>(256), granted)) return ITTT_ERR_CUDA;
-  return launch_clusters(kern, unsigned(std::min<long long>(tasks, (long long)ScanShape<T_>::CTAS * sms)), 1, kScanThreads,
-                         scan_smem_bytes<T_>(a.N), st, a, pl, g_wait_ns.load());
+  auto kern = scan_chunk_kernel<T_, P, STATE_ONLY>;
+  if (!grant_smem(kern, scan_smem_bytes<T_, P>(256), granted)) return ITTT_ERR_CUDA;
+  return launch_clusters(kern, unsigned(std::min<long long>(tasks, (long long)ScanShape<T_, P>::CTAS * sms)), 1, kScanThreads,
+                         scan_smem_bytes<T_, P>(a.N), st, a, pl, g_wait_ns.load());
+}
+
+template <typename T_, bool STATE_ONLY>
+ittt_status scan_chunks(const ScanArgs<T_>& a, const ScanPlan& pl, int passes, long long tasks, int sms,
+                        cudaStream_t st) {
+  if constexpr (sizeof(T_) == 2) {
+    if (passes == 2) return scan_chunks_wide<T_, 2, STATE_ONLY>(a, pl, tasks, sms, st);
+  }
+  return scan_chunks_wide<T_, 1, STATE_ONLY>(a, pl, tasks, sms, st);
 }
 
 template <typename T_>
@@ -496,14 +511,14 @@ ittt_status scan_launch(const ittt_scan_problem* p, const ScanArgs<T_>& a, void*
       if (cudaMemsetAsync(pl.flags, 0, size_t(1 + groups) * 4, st) != cudaSuccess) return ITTT_ERR_CUDA;
     } else {
       pl.step_sum = reinterpret_cast<float*>(ws + c.step_sum);
-      ittt_status s = scan_chunks<T_, true>(a, pl, groups * (c.runs - 1), sms, st);
+      ittt_status s = scan_chunks<T_, true>(a, pl, c.passes, groups * (c.runs - 1), sms, st);
       if (s != ITTT_OK) return s;
       s = launch_pdl(scan_join_kernel<T_>, dim3(unsigned(cdiv((long long)a.B * a.d * a.N, 256))),
                      dim3(256), st, a, pl);
       if (s != ITTT_OK) return s;
     }
   }
-  return scan_chunks<T_, false>(a, pl, groups * c.runs, sms, st);
+  return scan_chunks<T_, false>(a, pl, c.passes, groups * c.runs, sms, st);
 }
 
 }  // namespace

@@ -300,7 +300,11 @@ __global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs<T_> a, i
 // for 1667 tokens x 1000 x 32, 105 us with three.
 constexpr int kScanWarps = 4;
 constexpr int kScanThreads = 32 * kScanWarps;
-constexpr int kScanCh = 2 * kScanWarps;           // channels a CTA, two a warp
+// Channels a CTA: a warp takes P pairs of channels one after the other.  Two halve
+// what staging B and C costs a channel (8 x 1024 x 5120 x 16: 436 us, 474 with one);
+// one makes twice as many tasks (1 x 8192 x 5120: 470 us, 543 with two, whose 320
+// channel blocks leave CTAs without work).
+__host__ __device__ constexpr int scan_ch(int P) { return 2 * kScanWarps * P; }
 constexpr int kScanK = 8;                         // tokens a span, one span a lane
 constexpr int kScanChunk = 32 * kScanK;           // tokens a chunk
 constexpr int kScanJ = 2;                    // pairs of state elements at once
@@ -314,7 +318,7 @@ struct ScanPlan {
   int run_tokens;  // a multiple of kScanChunk
   int chained;     // 1: a run starts from the state that the run before leaves in
                    // `carry`; 0: run r from carry[r - 1] (filled by scan_join_kernel)
-  float* carry;    // chained: [B blocks][kScanCh NP]; else [runs - 1][B, d, N]
+  float* carry;    // chained: [B blocks][channels a block, NP]; else [runs - 1][B, d, N]
   float* step_sum; // state pass: [runs - 1][B, d], the runs' sums of s
   unsigned* flags; // chained: [0] the next task, [1 + B blocks] runs finished
 };
@@ -324,13 +328,14 @@ struct ScanPlan {
 // [pair of state elements][span][token], so that a lane reads the pair of 4 (or 2)
 // tokens with one 16-byte load; the spans stand 12 (20) words apart, which puts the
 // eight lanes of a quarter warp on different banks.
-template <typename T_>
+template <typename T_, int P>
 struct ScanShape {
+  static constexpr int CH = scan_ch(P);                      // channels
   static constexpr int ES = int(sizeof(T_));
   static constexpr int SLAB = 32 / ES;                       // state elements
   static constexpr int CTAS = ES == 2 ? 3 : 2;               // CTAs an SM
   static constexpr int PAIRS = SLAB / 2;
-  static constexpr int ROW_SPAN = kScanK * kScanCh + 16 / ES;  // elements between spans of raw rows
+  static constexpr int ROW_SPAN = kScanK * CH + 16 / ES;  // elements between spans of raw rows
   static constexpr int ROW_TILE = 32 * ROW_SPAN;
   static constexpr int PAIR_SPAN = kScanK * 2 * ES / 4 + 4;  // words between spans of laid out pairs
   static constexpr int PAIR_TILE = 32 * PAIR_SPAN;           // words of one pair
@@ -345,10 +350,11 @@ constexpr int kEndsSpan = 4 * kScanJ;                       // floats of a span'
 constexpr int kEndsGroup = kJoinSpans * kEndsSpan + kEndsSpan;  // the groups on different banks
 constexpr int kEndsWarp = 32 / kJoinSpans * kEndsGroup;
 __host__ __device__ constexpr int scan_np(int N) { return (N + 2 * kScanJ - 1) / (2 * kScanJ) * (2 * kScanJ); }
-template <typename T_>
+template <typename T_, int P>
 __host__ __device__ constexpr int scan_smem_bytes(int N) {
-  using S = ScanShape<T_>;
-  return S::ROWS + S::RAW + S::TILES + kScanWarps * kEndsWarp * 4 + 2 * kScanCh * scan_np(N) * 4;
+  using S = ScanShape<T_, P>;
+  return S::ROWS + S::RAW + S::TILES + kScanWarps * kEndsWarp * 4 + 2 * S::CH * scan_np(N) * 4 +
+         3 * S::CH * 4;
 }
 
 // 16 bytes global -> shared, not waited for; zeros where valid is false.
@@ -372,35 +378,35 @@ __device__ __forceinline__ bool pieces_ok(const T_* p, long long ld, int unit) {
 }
 
 // [tokens][nch] of one of U, delta, Z into a tile of rows (zeros elsewhere).
-template <typename T_>
+template <typename T_, int PASSES>
 __device__ __forceinline__ void fetch_rows(T_* tile, const T_* src, long long ld, int tokens, int nch,
                                            bool pieces) {
-  using S = ScanShape<T_>;
-  constexpr int V = 16 / S::ES, P = kScanCh / V;
+  using S = ScanShape<T_, PASSES>;
+  constexpr int V = 16 / S::ES, P = S::CH / V;
   if (pieces) {
 #pragma unroll
     for (int i = 0; i < kScanChunk * P / kScanThreads; ++i) {
       const int e = i * kScanThreads + static_cast<int>(threadIdx.x);
       const int t = e / P, c = (e % P) * V;
       const bool in = t < tokens && c < nch;
-      copy16_async(tile + (t / kScanK) * S::ROW_SPAN + (t % kScanK) * kScanCh + c,
+      copy16_async(tile + (t / kScanK) * S::ROW_SPAN + (t % kScanK) * S::CH + c,
                    src + (in ? t * ld + c : 0), in);
     }
   } else {
-    for (int e = threadIdx.x; e < kScanChunk * kScanCh; e += kScanThreads) {
-      const int t = e / kScanCh, c = e % kScanCh;
-      tile[(t / kScanK) * S::ROW_SPAN + (t % kScanK) * kScanCh + c] =
+    for (int e = threadIdx.x; e < kScanChunk * S::CH; e += kScanThreads) {
+      const int t = e / S::CH, c = e % S::CH;
+      tile[(t / kScanK) * S::ROW_SPAN + (t % kScanK) * S::CH + c] =
           (t < tokens && c < nch) ? src[t * ld + c] : from_f32<T_>(0.f);
     }
   }
 }
 
 // A tile of rows to Y: the counterpart of fetch_rows.
-template <typename T_>
+template <typename T_, int PASSES>
 __device__ __forceinline__ void store_rows(T_* dst, const T_* tile, long long ld, int tokens, int nch,
                                            bool pieces) {
-  using S = ScanShape<T_>;
-  constexpr int V = 16 / S::ES, P = kScanCh / V;
+  using S = ScanShape<T_, PASSES>;
+  constexpr int V = 16 / S::ES, P = S::CH / V;
   if (pieces) {
 #pragma unroll
     for (int i = 0; i < kScanChunk * P / kScanThreads; ++i) {
@@ -408,23 +414,23 @@ __device__ __forceinline__ void store_rows(T_* dst, const T_* tile, long long ld
       const int t = e / P, c = (e % P) * V;
       if (t < tokens && c < nch)
         *reinterpret_cast<uint4*>(dst + t * ld + c) = *reinterpret_cast<const uint4*>(
-            tile + (t / kScanK) * S::ROW_SPAN + (t % kScanK) * kScanCh + c);
+            tile + (t / kScanK) * S::ROW_SPAN + (t % kScanK) * S::CH + c);
     }
   } else {
-    for (int e = threadIdx.x; e < kScanChunk * kScanCh; e += kScanThreads) {
-      const int t = e / kScanCh, c = e % kScanCh;
+    for (int e = threadIdx.x; e < kScanChunk * S::CH; e += kScanThreads) {
+      const int t = e / S::CH, c = e % S::CH;
       if (t < tokens && c < nch)
-        dst[t * ld + c] = tile[(t / kScanK) * S::ROW_SPAN + (t % kScanK) * kScanCh + c];
+        dst[t * ld + c] = tile[(t / kScanK) * S::ROW_SPAN + (t % kScanK) * S::CH + c];
     }
   }
 }
 
 // The slab [n0, n0 + SLAB) of B or C of a chunk's tokens, as it comes: [token][SLAB]
 // (zeros behind the end and past N).
-template <typename T_>
+template <typename T_, int PASSES>
 __device__ __forceinline__ void fetch_slab(T_* dst, const T_* src, long long ld, int tokens, int N,
                                            int n0, bool pieces) {
-  using S = ScanShape<T_>;
+  using S = ScanShape<T_, PASSES>;
   constexpr int V = 16 / S::ES;
   if (pieces) {
 #pragma unroll
@@ -443,9 +449,9 @@ __device__ __forceinline__ void fetch_slab(T_* dst, const T_* src, long long ld,
 }
 
 // [token][SLAB] -> [pair][span][token].
-template <typename T_>
+template <typename T_, int PASSES>
 __device__ __forceinline__ void lay_out(uint32_t* tile, const T_* raw) {
-  using S = ScanShape<T_>;
+  using S = ScanShape<T_, PASSES>;
 #pragma unroll
   for (int t = threadIdx.x; t < kScanChunk; t += kScanThreads) {
     const uint4* src = reinterpret_cast<const uint4*>(raw + t * S::SLAB);
@@ -505,10 +511,10 @@ __device__ __forceinline__ void store_two(float* p, float x, float y) {
 
 // STATE_ONLY: the first of the two passes of a call that is split over time: every
 // run from a zero state, its end state and sum of steps written, no outputs.
-template <typename T_, bool STATE_ONLY>
-__global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
+template <typename T_, int P, bool STATE_ONLY>
+__global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
     scan_chunk_kernel(const ScanArgs<T_> a, const ScanPlan pl, unsigned long long wait_ns) {
-  using S = ScanShape<T_>;
+  using S = ScanShape<T_, P>;
   extern __shared__ __align__(16) uint8_t scan_smem[];
   const int NP = scan_np(a.N);
   T_* rows = reinterpret_cast<T_*>(scan_smem);                        // U, delta, Z (then Y)
@@ -516,7 +522,10 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
   uint32_t* tiles = reinterpret_cast<uint32_t*>(scan_smem + S::ROWS + S::RAW);
   float* ends_all = reinterpret_cast<float*>(scan_smem + S::ROWS + S::RAW + S::TILES);
   float* state = ends_all + kScanWarps * kEndsWarp;                            // [ch][NP]
-  float* A2s = state + kScanCh * NP;                                  // [ch][NP], A log2(e)
+  float* A2s = state + S::CH * NP;                                  // [ch][NP], A log2(e)
+  float* biases = A2s + S::CH * NP;                                 // [ch]
+  float* skips = biases + S::CH;                                    // [ch]
+  float* totals = skips + S::CH;                                    // [ch], STATE_ONLY: sums of s
   __shared__ int next_task, aborted;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -531,8 +540,7 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
   float* my_end = ends + (lane / kJoinSpans) * kEndsGroup + (lane % kJoinSpans) * kEndsSpan;
   const int q = lane % kEndsSpan, first_span = lane / kEndsSpan * kJoinSpans;
   float* join_ends = ends + (lane / kEndsSpan) * kEndsGroup + q;
-  float* join_state = state + (2 * warp + (q & 1)) * NP + (q >> 1);
-  const float* join_A2 = A2s + (2 * warp + (q & 1)) * NP + (q >> 1);
+  const int join_at = (q & 1) * NP + (q >> 1);
   if (tid == 0) aborted = 0;
   grid_dependency_wait();
 
@@ -552,9 +560,9 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
     const int run = task / groups, gb = task - run * groups;
     const int b = gb / pl.blocks, blk = gb - b * pl.blocks;
     const int g = blk / pl.per_group;
-    const int in_group = (blk - g * pl.per_group) * kScanCh;
+    const int in_group = (blk - g * pl.per_group) * S::CH;
     const int c0 = g * dg + in_group;
-    const int nch = min(kScanCh, dg - in_group);
+    const int nch = min(S::CH, dg - in_group);
     const int len = sequence_length(a.lengths, b, a.T);
     const int t_begin = run * pl.run_tokens;
     const int t_end = min(len, t_begin + pl.run_tokens);
@@ -573,15 +581,15 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
     auto fetch_inputs = [&](int t0) {
       const int tokens = min(kScanChunk, t_end - t0);
       const long long row = row0 + t0;
-      fetch_rows(rows, a.U + row * a.ldu + c0, a.ldu, tokens, nch, pieces_u);
-      fetch_rows(rows + S::ROW_TILE, a.delta + row * a.ldt + c0, a.ldt, tokens, nch, pieces_t);
+      fetch_rows<T_, P>(rows, a.U + row * a.ldu + c0, a.ldu, tokens, nch, pieces_u);
+      fetch_rows<T_, P>(rows + S::ROW_TILE, a.delta + row * a.ldt + c0, a.ldt, tokens, nch, pieces_t);
     };
     auto fetch_bc = [&](int t0, int n0) {
       const int tokens = min(kScanChunk, t_end - t0);
       const long long row = row0 + t0, gn = (long long)g * a.N;
-      fetch_slab(raw, a.Bm + row * a.ldb + gn, a.ldb, tokens, a.N, n0, pieces_b);
+      fetch_slab<T_, P>(raw, a.Bm + row * a.ldb + gn, a.ldb, tokens, a.N, n0, pieces_b);
       if (!STATE_ONLY)
-        fetch_slab(raw + kScanChunk * S::SLAB, a.Cm + row * a.ldc + gn, a.ldc, tokens, a.N, n0, pieces_c);
+        fetch_slab<T_, P>(raw + kScanChunk * S::SLAB, a.Cm + row * a.ldc + gn, a.ldc, tokens, a.N, n0, pieces_c);
     };
     if (t_begin < t_end) {
       fetch_inputs(t_begin);
@@ -600,7 +608,7 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
         return;
       }
     }
-    for (int e = tid; e < kScanCh * NP; e += kScanThreads) {
+    for (int e = tid; e < S::CH * NP; e += kScanThreads) {
       const int i = e / NP, n = e - i * NP;
       float h = 0.f, A2 = 0.f;
       if (i < nch && n < a.N) {
@@ -608,7 +616,7 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
         const long long at = ((long long)b * a.d + c0 + i) * a.N + n;
         if (!STATE_ONLY) {
           if (first) h = a.state_in ? a.state_in[at] : 0.f;
-          else if (pl.chained) h = __ldcg(pl.carry + ((long long)gb * kScanCh + i) * NP + n);
+          else if (pl.chained) h = __ldcg(pl.carry + ((long long)gb * S::CH + i) * NP + n);
           else h = pl.carry[(long long)(run - 1) * a.B * a.d * a.N + at];
         }
       }
@@ -616,19 +624,12 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
       A2s[e] = A2;
     }
 
-    // this thread's two channels (past nch: zeros in, nothing out)
-    const int ch = 2 * warp;
-    float2 bias = make_float2(0.f, 0.f), skip = make_float2(0.f, 0.f);
-    if (a.dt_bias) {
-      if (ch < nch) bias.x = a.dt_bias[c0 + ch];
-      if (ch + 1 < nch) bias.y = a.dt_bias[c0 + ch + 1];
+    if (tid < S::CH) {
+      biases[tid] = (a.dt_bias && tid < nch) ? a.dt_bias[c0 + tid] : 0.f;
+      skips[tid] = (a.D && tid < nch) ? a.D[c0 + tid] : 0.f;
+      totals[tid] = 0.f;
     }
-    if (a.D) {
-      if (ch < nch) skip.x = a.D[c0 + ch];
-      if (ch + 1 < nch) skip.y = a.D[c0 + ch + 1];
-    }
-    float2 steps_total = make_float2(0.f, 0.f);  // STATE_ONLY: this lane's share of the run's sums of s
-    const T_* my_rows = rows + lane * S::ROW_SPAN + ch;
+    const bool one_slab = NP <= S::SLAB;
 
     for (int t0 = t_begin; t0 < t_end; t0 += kScanChunk) {
       const int tokens = min(kScanChunk, t_end - t0);
@@ -638,19 +639,33 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
       float2 su[kScanK];
       float join_sum[kJoinSpans];       // sums of s of the spans that this lane joins
 
+#pragma unroll 1
+      for (int pass = 0; pass < P; ++pass) {
+      // this thread's two channels (past nch: zeros in, nothing out)
+      const int ch = 2 * (warp + kScanWarps * pass);
+      const T_* my_rows = rows + lane * S::ROW_SPAN + ch;
+      float* join_state = state + ch * NP + join_at;
+      const float* join_A2 = A2s + ch * NP + join_at;
+      const bool last_pass = pass == P - 1;
+#pragma unroll 1
       for (int n0 = 0; n0 < NP; n0 += S::SLAB) {
-        copy_wait<0>();
-        __syncthreads();  // the copies are in; the tiles' readers of the step before are done
+        const bool fresh = pass == 0 || !one_slab;  // else B and C are laid out already
+        if (fresh) {
+          copy_wait<0>();
+          __syncthreads();  // the copies are in; the tiles' readers of the step before are done
+        }
         if (n0 == 0) {
-          if (!STATE_ONLY && a.Z) {
-            fetch_rows(rows + 2 * S::ROW_TILE, a.Z + (row0 + t0) * a.ldz + c0, a.ldz, tokens, nch, pieces_z);
+          if (!STATE_ONLY && a.Z && pass == 0) {
+            fetch_rows<T_, P>(rows + 2 * S::ROW_TILE, a.Z + (row0 + t0) * a.ldz + c0, a.ldz, tokens, nch, pieces_z);
             copy_commit();
           }
+          const float2 bias = *reinterpret_cast<const float2*>(biases + ch);
+          const float2 skip = *reinterpret_cast<const float2*>(skips + ch);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < kScanK; ++k) {
-            const float2 u = load_two(my_rows + k * kScanCh);
-            float2 s = load_two(my_rows + S::ROW_TILE + k * kScanCh);
+            const float2 u = load_two(my_rows + k * S::CH);
+            float2 s = load_two(my_rows + S::ROW_TILE + k * S::CH);
             s.x += bias.x;
             s.y += bias.y;
             if (a.softplus) {
@@ -671,17 +686,29 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
             const float z = __shfl_sync(0xffffffffu, sum.y, first_span + i);
             join_sum[i] = (q & 1) ? z : x;
           }
-          if (STATE_ONLY) {
-            steps_total.x += sum.x;
-            steps_total.y += sum.y;
+          if constexpr (STATE_ONLY) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+              sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+              sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+            }
+            if (lane == 0) {
+              totals[ch] += sum.x;
+              totals[ch + 1] += sum.y;
+            }
           }
         }
-        lay_out(tiles, raw);
-        if (!STATE_ONLY) lay_out(tiles + S::PAIRS * S::PAIR_TILE, raw + kScanChunk * S::SLAB);
-        __syncthreads();
+        if (fresh) {
+          lay_out<T_, P>(tiles, raw);
+          if (!STATE_ONLY) lay_out<T_, P>(tiles + S::PAIRS * S::PAIR_TILE, raw + kScanChunk * S::SLAB);
+        }
+        // before the tiles are read, and before the rows, read above by all, are replaced
+        if (fresh || last_pass) __syncthreads();
         // what comes next arrives during the recurrences
         if (n0 + S::SLAB < NP) {
           fetch_bc(t0, n0 + S::SLAB);
+        } else if (!last_pass) {
+          if (!one_slab) fetch_bc(t0, 0);
         } else if (t0 + kScanChunk < t_end) {
           fetch_inputs(t0 + kScanChunk);
           fetch_bc(t0 + kScanChunk, 0);
@@ -786,37 +813,34 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
       }
 
       if (!STATE_ONLY) {
-        copy_wait<1>();   // Z is in (the next step's copies may still run)
-        __syncthreads();
+        if (pass == 0) {
+          copy_wait<1>();   // Z is in (the next step's copies may still run)
+          __syncthreads();
+        }
         T_* zy = const_cast<T_*>(my_rows) + 2 * S::ROW_TILE;  // Z's place becomes Y's
 #pragma unroll
         for (int k = 0; k < kScanK; ++k) {
           float y0, y1;
           unpack2(y2[k], y0, y1);
           if (a.Z) {
-            const float2 z = load_two(zy + k * kScanCh);
+            const float2 z = load_two(zy + k * S::CH);
             y0 *= silu_fast(z.x);
             y1 *= silu_fast(z.y);
           }
-          store_two(zy + k * kScanCh, y0, y1);
+          store_two(zy + k * S::CH, y0, y1);
         }
+      }
+      }
+      if (!STATE_ONLY) {
         __syncthreads();
-        store_rows(a.Y + (row0 + t0) * a.ldy + c0, rows + 2 * S::ROW_TILE, a.ldy, tokens, nch, pieces_y);
+        store_rows<T_, P>(a.Y + (row0 + t0) * a.ldy + c0, rows + 2 * S::ROW_TILE, a.ldy, tokens, nch, pieces_y);
       }
     }
 
     __syncthreads();  // the state of the run's last token is complete
     if (STATE_ONLY) {
       const long long at = ((long long)run * a.B + b) * a.d + c0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        steps_total.x += __shfl_xor_sync(0xffffffffu, steps_total.x, o);
-        steps_total.y += __shfl_xor_sync(0xffffffffu, steps_total.y, o);
-      }
-      if (lane == 0) {
-        if (ch < nch) pl.step_sum[at + ch] = steps_total.x;
-        if (ch + 1 < nch) pl.step_sum[at + ch + 1] = steps_total.y;
-      }
+      if (tid < nch) pl.step_sum[at + tid] = totals[tid];
       for (int e = tid; e < nch * a.N; e += kScanThreads)
         pl.carry[at * a.N + e] = state[(e / a.N) * NP + e % a.N];
       continue;
@@ -826,8 +850,8 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_>::CTAS)
         for (int e = tid; e < nch * a.N; e += kScanThreads)
           a.state_out[((long long)b * a.d + c0) * a.N + e] = state[(e / a.N) * NP + e % a.N];
     } else if (pl.chained) {
-      for (int e = tid; e < kScanCh * NP; e += kScanThreads)
-        pl.carry[(long long)gb * kScanCh * NP + e] = state[e];
+      for (int e = tid; e < S::CH * NP; e += kScanThreads)
+        pl.carry[(long long)gb * S::CH * NP + e] = state[e];
       __threadfence();
       __syncthreads();
       if (tid == 0) red_release_gpu_add(pl.flags + 1 + gb, 1u);
