@@ -42,7 +42,9 @@ def check(Y, X, W, b, R, act, dtype):
 SHAPES = [(1, 8, 1), (1, 2560, 640), (2, 64, 33), (7, 520, 130), (8, 1024, 24), (9, 128, 256),
           (16, 72, 65), (17, 2568, 192), (33, 256, 1000), (64, 520, 264), (65, 192, 40),
           (127, 64, 129), (128, 128, 128), (129, 136, 257), (255, 2048, 192), (257, 640, 512),
-          (600, 320, 776), (1100, 256, 1032)]
+          (600, 320, 776), (1100, 256, 1032),
+          (1700, 72, 1400), (2500, 136, 1033), (129, 8, 9500),    # CTA pairs
+          (200, 2560, 10304)]                                    # pairs, W beyond L2's share
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -56,7 +58,8 @@ def test_product(M, K, N, dtype):
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("M,K,N,dtype", [(1, 256, 72, "bf16"), (5, 256, 71, "bf16"),
                                          (40, 256, 100, "bf16"), (300, 256, 520, "bf16"),
-                                         (50, 37, 61, "f32"), (1, 37, 61, "f32")])
+                                         (1700, 64, 1400, "bf16"), (50, 37, 61, "f32"),
+                                         (1, 37, 61, "f32"), (1700, 20, 1400, "f32")])
 def test_activations(act, M, K, N, dtype):
     X, W, b, R = make(M, K, N, dtype, seed=1)
     check(ittt.linear(X, W, b, act=act), X, W, b, None, act, dtype)
@@ -64,8 +67,8 @@ def test_activations(act, M, K, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("M", [1, 3, 20, 150, 700])
-@pytest.mark.parametrize("N", [64, 130, 251])
+@pytest.mark.parametrize("M,N", [(m, n) for m in (1, 3, 20, 150, 700) for n in (64, 130, 251)] +
+                         [(2300, 1290), (5000, 517)])
 def test_strides(dtype, M, N):
     """X, residual and Y as column slices of wider matrices; what stands beside
     Y's columns stays; in place on the residual."""
@@ -83,9 +86,9 @@ def test_strides(dtype, M, N):
     assert Y3.shape == (1, M, N)
 
 
-@pytest.mark.parametrize("M", [1, 4, 24, 200])
-def test_nan_and_inf_stay_in_their_rows(M):
-    X, W, b, R = make(M, 128, 200, "bf16", seed=3)
+@pytest.mark.parametrize("M,N", [(1, 200), (4, 200), (24, 200), (200, 200), (2000, 1300)])
+def test_nan_and_inf_stay_in_their_rows(M, N):
+    X, W, b, R = make(M, 128, N, "bf16", seed=3)
     X[M // 2, 7] = float("nan")
     Y = ittt.linear(X, W, b, R, act="silu")
     bad = torch.isnan(Y).all(dim=1)

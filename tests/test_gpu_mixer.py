@@ -206,6 +206,7 @@ def test_scan_nan_stays_in_its_channel_and_later_tokens():
 
 
 @pytest.mark.parametrize("B,T,d,N,dtype", [(1, 3000, 16, 16, "f32"), (2, 1500, 24, 8, "bf16"),
+                                           (1, 900, 40, 256, "bf16"), (1, 700, 16, 130, "f32"),
                                            (1, 2100, 20, 33, "f32")])
 def test_scan_long_and_narrow(B, T, d, N, dtype):
     """Few channels and many tokens: the scan is split over time."""
@@ -225,6 +226,23 @@ def test_scan_long_and_wide(dtype, lengths):
     Y, s = check_scan(v, dtype, lengths=n, out=out)
     Y2, s2 = ittt.selective_scan(**v, lengths=n, out=None if out is None else out.clone())
     assert torch.equal(Y, Y2) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("B,T,d,N,G,lengths", [
+    (8, 300, 900, 4, 1, None),
+    (8, 280, 904, 16, 2, None),                                        # grouped projections
+    (8, 300, 909, 5, 1, None),                                         # rows without 16-byte pieces
+    (8, 1300, 900, 3, 1, [1300, 1025, 1024, 0, 1, 256, 257, 700]),     # runs handed on
+    (1, 28500, 250, 4, 1, None),                                       # independent runs
+])
+def test_scan_many_channels(B, T, d, N, G, lengths):
+    """Enough work for the wider channel blocks (two passes of channels a CTA)."""
+    v = scan_inputs(B, T, d, N, G, "bf16", seed=11)
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out = None if lengths is None else torch.full_like(v["U"], 5.0)
+    Y, s = check_scan(v, "bf16", lengths=n, out=out)
+    v["Z"] = v["D"] = v["state"] = None
+    check_scan(v, "bf16", lengths=n, out=None if out is None else torch.full_like(out, 5.0))
 
 
 @pytest.mark.parametrize("cuts", [[1], [7, 8], [64, 200], [128]])
