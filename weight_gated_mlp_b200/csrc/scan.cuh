@@ -5,8 +5,8 @@
 // One exponential per state element and token is the largest cost (the unit that
 // computes it takes 16 a clock and SM), so no kernel computes one twice.
 //
-//   scan_token_kernel   single tokens: lanes over the state, several sequences a
-//       thread.  Bound by the state's bytes.
+//   scan_token_kernel   single tokens: lanes over the state, sequence after sequence.
+//       Bound by the state's bytes.
 //   scan_serial_kernel  short calls: lanes over the state, four or eight elements a
 //       lane, four tokens at a time.
 //   scan_chunk_kernel   prompts: 8 channels a CTA, 256 tokens at a time.  A
@@ -216,75 +216,77 @@ __global__ void __launch_bounds__(128) scan_serial_kernel(const ScanArgs<T_> a, 
   }
 }
 
-// Single tokens (N <= 128): four state elements a lane of one channel, for SEQ
-// sequences at once, so that A is read once for them and SEQ times as many bytes
-// of state are in flight.  Bound by reading and writing the state.
-template <typename T_, int SEQ, bool VEC>
+// Single tokens (N <= 128): four state elements a lane of one channel.  A thread keeps
+// its channel (A, D and the bias are read once) and walks over the sequences
+// blockIdx.y, blockIdx.y + gridDim.y, ..., the next one's loads under way while one is
+// computed.  Bound by reading and writing the state.
+template <typename T_, bool VEC>
 __global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs<T_> a, int lanes) {
   grid_dependency_wait();
-  const long long gid = (blockIdx.x * 128ll + threadIdx.x) / lanes;
+  const int gid = static_cast<int>((blockIdx.x * 128ll + threadIdx.x) / lanes);
   const int sub = threadIdx.x & (lanes - 1);
-  const int batches = (a.B + SEQ - 1) / SEQ;
   // every thread of a warp stays for the shuffles; those past the end repeat the last channel
-  const bool real = gid < (long long)batches * a.d;
-  const long long w = real ? gid : (long long)batches * a.d - 1;
-  const int b0 = static_cast<int>(w / a.d) * SEQ, c = static_cast<int>(w - (w / a.d) * a.d);
+  const bool real = gid < a.d;
+  const int c = real ? gid : a.d - 1;
   const int g = c / (a.d / a.G);
   const int live = a.N - 4 * sub;                 // elements of this lane's quad (may be <= 0)
   const int n0 = live > 0 ? 4 * sub : 0, some = live > 0 ? live : a.N;
   const long long cn = (long long)c * a.N + n0, gn = (long long)g * a.N + n0;
-  Quad<float> A, h[SEQ];
-  Quad<T_> Bq[SEQ], Cq[SEQ];
-  T_ u[SEQ], s[SEQ], z[SEQ];
-  int len[SEQ];
   const T_* zp = a.Z ? a.Z : a.U;  // a row of something where there is no gate
   const long long ldz = a.Z ? a.ldz : a.ldu;
   const float* sp = a.state_in ? a.state_in : a.A;
-  const float from_state = a.state_in ? 1.f : 0.f;
-#pragma unroll
-  for (int i = 0; i < SEQ; ++i) {
-    const long long row = min(b0 + i, a.B - 1);  // past the batch: the last sequence again
-    h[i].template load<VEC>(sp + (a.state_in ? row * a.d * a.N + cn : cn), some);
-    Bq[i].template load<VEC>(a.Bm + row * a.ldb + gn, some);
-    Cq[i].template load<VEC>(a.Cm + row * a.ldc + gn, some);
-    u[i] = a.U[row * a.ldu + c];
-    s[i] = a.delta[row * a.ldt + c];
-    z[i] = zp[row * ldz + c];
-    len[i] = a.lengths ? a.lengths[row] : 1;
-  }
+  const long long sequence = a.state_in ? (long long)a.d * a.N : 0;
+  struct Item {
+    Quad<float> h;
+    Quad<T_> B, C;
+    T_ u, s, z;
+    int len;
+  } next;
+  auto load = [&](int b) {
+    const long long row = min(b, a.B - 1);  // past the batch: the last sequence again
+    next.h.template load<VEC>(sp + row * sequence + cn, some);
+    next.B.template load<VEC>(a.Bm + row * a.ldb + gn, some);
+    next.C.template load<VEC>(a.Cm + row * a.ldc + gn, some);
+    next.u = a.U[row * a.ldu + c];
+    next.s = a.delta[row * a.ldt + c];
+    next.z = zp[row * ldz + c];
+    next.len = a.lengths ? a.lengths[row] : 1;
+  };
+  load(blockIdx.y);
+  Quad<float> A;
   A.load<VEC>(a.A + cn, some);
   const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
   const float skip = a.D ? a.D[c] : 0.f;
-#pragma unroll
-  for (int i = 0; i < SEQ; ++i) {
-    const bool in = real && b0 + i < a.B, on = in && len[i] > 0;
-    const float uf = to_f32(u[i]);
-    float st = to_f32(s[i]) + bias;
+  for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+    Item now = next;
+    load(b + gridDim.y);
+    const bool on = real && now.len > 0;
+    const float uf = to_f32(now.u);
+    float st = to_f32(now.s) + bias;
     if (a.softplus) st = softplus_f32(st);
     const float su = st * uf;
     float y = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float before = from_state != 0.f ? h[i].v[j] : 0.f;
-      const float next = fmaf(exp2_approx(st * (A.v[j] * kLog2e)), before, su * to_f32(Bq[i].v[j]));
-      if (j < live) y = fmaf(next, to_f32(Cq[i].v[j]), y);
-      h[i].v[j] = on ? next : before;  // an empty sequence passes its state through
+      const float before = a.state_in ? now.h.v[j] : 0.f;
+      const float after = fmaf(exp2_approx(st * (A.v[j] * kLog2e)), before, su * to_f32(now.B.v[j]));
+      if (j < live) y = fmaf(after, to_f32(now.C.v[j]), y);
+      now.h.v[j] = on ? after : before;  // an empty sequence passes its state through
     }
     for (int o = lanes >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-    const long long row = b0 + i;
     if (on && sub == 0) {
       if (a.D) y = fmaf(skip, uf, y);
-      if (a.Z) y *= silu_fast(to_f32(z[i]));
-      a.Y[row * a.ldy + c] = from_f32<T_>(y);
+      if (a.Z) y *= silu_fast(to_f32(now.z));
+      a.Y[b * a.ldy + c] = from_f32<T_>(y);
     }
-    if (a.state_out && in) {
-      float* p = a.state_out + row * a.d * a.N + cn;
+    if (a.state_out && real) {
+      float* p = a.state_out + (long long)b * a.d * a.N + cn;
       if (VEC && live > 0) {
-        *reinterpret_cast<Quad<float>*>(p) = h[i];
+        *reinterpret_cast<Quad<float>*>(p) = now.h;
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (j < live) p[j] = h[i].v[j];
+          if (j < live) p[j] = now.h.v[j];
       }
     }
   }
