@@ -81,6 +81,18 @@ ittt_status launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned clus
   return launch_status();
 }
 
+// Dynamic shared memory above the default, granted once per kernel and device.
+template <typename Kern>
+bool grant_smem(Kern kern, int smem, std::atomic<bool>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if (done[dev].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return false;
+  done[dev].store(true, std::memory_order_relaxed);
+  return true;
+}
+
 template <int ACT, int MB, bool VEC>
 ittt_status linear_gemv(const LinearArgs<float>& a, cudaStream_t st) {
   return launch_pdl(linear_gemv_kernel<ACT, MB, VEC>, dim3(unsigned(cdiv(a.N, 4))), dim3(128), st, a);
@@ -119,16 +131,13 @@ ittt_status linear_f32(const LinearArgs<float>& a, cudaStream_t st) {
   return linear_f32_sized<ACT, false>(a, sms, st);
 }
 
-// Dynamic shared memory above the default, granted once per kernel and device.
-template <typename Kern>
-bool grant_smem(Kern kern, int smem, std::atomic<bool>* done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-  if (done[dev].load(std::memory_order_relaxed)) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return false;
-  done[dev].store(true, std::memory_order_relaxed);
-  return true;
+// Dynamic shared memory that spreads `ctas` CTAs evenly: as much as lets no SM hold more
+// of them than the fullest one has to.  Clusters are otherwise packed onto fewer SMs
+// (777 x 5120 x 192, 208 CTAs: 8.6 us, 10.1 without).
+int spread_smem(long long ctas, int sms, int need) {
+  const long long per_sm = std::max(1ll, cdiv(ctas, sms));
+  const long long share = 233472 / per_sm - 1024;  // an SM's shared memory; 1 KB a CTA is reserved
+  return int(std::max<long long>(need, std::min<long long>(share, 232448) / 1024 * 1024));
 }
 
 // One 128 x MT tile per CTA, K split over clusters.  The split is the widest of
@@ -139,7 +148,7 @@ ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream
   using S = SplitShape<MT>;
   static std::atomic<bool> granted[kMaxDevices] = {};
   auto kern = linear_split_kernel<MT, ACT>;
-  if (!grant_smem(kern, S::SMEM, granted)) return ITTT_ERR_CUDA;
+  if (!grant_smem(kern, 232448, granted)) return ITTT_ERR_CUDA;
   const int num_kb = int(cdiv(a.K, 64));
   const long long m_tiles = cdiv(a.M, MT), tiles = m_tiles * cdiv(a.N, 128);
   int splits = 1;
@@ -148,7 +157,8 @@ ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream
   CUtensorMap w, x;
   if (!make_map(&w, a.W, a.K, a.N, a.K, 64, 128) || !make_map(&x, a.X, a.K, a.M, a.ldx, 64, MT))
     return ITTT_ERR_CUDA;
-  return launch_clusters(kern, unsigned(tiles * splits), unsigned(splits), 192, S::SMEM, st, w, x, a,
+  return launch_clusters(kern, unsigned(tiles * splits), unsigned(splits), 192,
+                         spread_smem(tiles * splits, sms, S::SMEM), st, w, x, a,
                          int(m_tiles), num_kb, g_wait_ns.load());
 }
 
