@@ -427,8 +427,8 @@ typedef struct {
 /* Y = act(X W^T + bias) + residual.
  * X [M, K]; W [N, K] (nn.Linear layout); bias [N] or NULL; residual [M, N] or
  * NULL, may be Y itself (with ldr = ldy) and must not overlap Y otherwise;
- * Y [M, N], which must not overlap X, W or bias.  Sums are held in fp32 and the epilogue computes in fp32 with one
- * rounding on the store.  bf16: K % 8 == 0, ldx % 8 == 0, X and W 16-byte
+ * Y [M, N], which must not overlap X, W or bias.  Sums are held in fp32 and the
+ * epilogue computes in fp32 with one rounding on the store.  bf16: K % 8 == 0, ldx % 8 == 0, X and W 16-byte
  * aligned (else ITTT_ERR_UNSUPPORTED); M, N, ldr and ldy are free.  f32: any
  * sizes.  The result does not depend on what ran before or beside the call. */
 ittt_status ittt_linear(const ittt_linear_problem* p, const void* X, const void* W,
@@ -456,7 +456,8 @@ typedef struct {
  * conv_kernel [d, k]; bias [d] or NULL; lengths: int32 [B] on the device or
  * NULL: sequence b has lengths[b] tokens in this call (clamped to 0..T); the
  * rows behind them are not read, and their rows of Y are left as they were.
- * Y must not overlap X or the states.  One rounding, on the store. */
+ * Y must not overlap another tensor, state_out none but state_in.  One rounding, on
+ * the store. */
 ittt_status ittt_causal_conv(const ittt_conv_problem* p, const void* X, const void* conv_kernel,
                              const void* bias, const void* state_in, const int32_t* lengths,
                              void* Y, void* state_out, void* stream);
@@ -478,7 +479,7 @@ typedef struct {
 } ittt_scan_problem;
 
 /* Bytes of workspace ittt_selective_scan needs for *p on the current device (0
- * unless the call is split over time: few channels and many tokens).
+ * unless the call is cut over time).
  * Validates *p like the call. */
 ittt_status ittt_selective_scan_workspace_size(const ittt_scan_problem* p, size_t* bytes);
 
@@ -492,7 +493,8 @@ ittt_status ittt_selective_scan_workspace_size(const ittt_scan_problem* p, size_
  * float32 (NULL: zeros) is h before the call's first token, state_out [B, d, N]
  * float32 (NULL: not wanted) h after each sequence's last one, and may be
  * state_in itself.  lengths as for ittt_causal_conv (a sequence of length 0
- * passes its state through).  Y must not overlap an input.  Everything is
+ * passes its state through).  Y must not overlap another tensor, state_out none but
+ * state_in.  Everything is
  * computed and held in fp32; Y is rounded once.  Made for decay, s A <= 0: where
  * s A > 0, the growth over any 256 tokens has to stay within fp32's range, and
  * what leaves that range comes out inf or NaN. */

@@ -81,6 +81,11 @@ def test_conv_pointers(lib):
     assert lib.ittt_causal_conv(r, FAKE, FAKE, None, None, None, FAKE, None, None) == INV  # Y = X
     assert lib.ittt_causal_conv(r, FAKE, FAKE, None, other, None, other, None, None) == INV
     assert lib.ittt_causal_conv(r, FAKE, FAKE, None, None, None, other, other, None) == INV
+    x, w, bias, y = (ctypes.c_void_p(n << 22) for n in range(1, 5))
+    for out in (w, bias):
+        assert lib.ittt_causal_conv(r, x, w, bias, None, None, out, None, None) == INV
+    for state_out in (x, w, bias):
+        assert lib.ittt_causal_conv(r, x, w, bias, None, None, y, state_out, None) == INV
 
 
 def _scan(**kw):
@@ -95,6 +100,7 @@ def _scan(**kw):
     (dict(G=3), INV), (dict(N=257), UNS), (dict(dtype=-1), INV), (dict(flags=2), INV),
     (dict(ldu=15), INV), (dict(ldt=1), INV), (dict(ldb=15), INV), (dict(ldc=8), INV),
     (dict(ldz=-16), INV), (dict(ldy=4), INV), (dict(B=1 << 16, T=1 << 15), UNS),
+    (dict(B=(1 << 30) + 1, T=1, d=1, N=1, G=1), UNS),
 ])
 def test_scan_problems(lib, kw, status):
     p, n, other = _scan(**kw), ctypes.c_size_t(0), ctypes.c_void_p(1 << 21)
@@ -115,6 +121,14 @@ def test_scan_pointers(lib):
     assert lib.ittt_selective_scan(r, *[FAKE] * 5, None, None, None, None, None, FAKE, None, None, 0,
                                    None) == INV  # Y = U
     assert lib.ittt_selective_scan_workspace_size(r, None) == INV
+    # no output may be another tensor (but state_out state_in)
+    u, delta, a, bm, cm, d, bias, z, state, y = (ctypes.c_void_p(n << 22) for n in range(1, 11))
+    for out in (u, delta, a, bm, cm, d, bias, z, state):
+        assert lib.ittt_selective_scan(r, u, delta, a, bm, cm, d, bias, z, state, None, out, None, None,
+                                       0, None) == INV
+    for out in (u, delta, a, bm, cm, d, bias, z, y):
+        assert lib.ittt_selective_scan(r, u, delta, a, bm, cm, d, bias, z, state, None, y, out, None, 0,
+                                       None) == INV
 
 
 def test_rows_of_a_view():

@@ -2,11 +2,13 @@
 // tensor cores' TF32 does not keep fp32's precision).
 //
 //   linear_gemv_kernel  up to 8 rows of X: a CTA's four warps share four rows of W
-//       and split K; W streams from HBM once, 16 bytes a lane.
+//       and split K; W streams from HBM once, 16 bytes a lane.  Bound by W's bytes.
 //   linear_f32_kernel   BM x BN tiles, TM x TN outputs a thread, the next 16
 //       columns of K in registers while the present ones are multiplied.  The
 //       CTAs of a cluster split K where there are few tiles and join their sums
-//       through distributed shared memory, in rank order.
+//       through distributed shared memory, in rank order.  Bound by the CUDA cores and
+//       the shared-memory reads that feed them: 333 x 1000 x 1001 with bias and gelu
+//       28.3 us (9.0 us at 128 products a clock and SM).
 #pragma once
 
 #include "common.cuh"

@@ -227,9 +227,13 @@ ittt_status linear_bf16(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
 }
 
 template <int ACT>
-ittt_status linear_typed(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) { return linear_bf16<ACT>(a, st); }
+ittt_status linear_typed(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
+  return linear_bf16<ACT>(a, st);
+}
 template <int ACT>
-ittt_status linear_typed(const LinearArgs<float>& a, cudaStream_t st) { return linear_f32<ACT>(a, st); }
+ittt_status linear_typed(const LinearArgs<float>& a, cudaStream_t st) {
+  return linear_f32<ACT>(a, st);
+}
 
 template <typename T_>
 ittt_status linear_by_act(const LinearArgs<T_>& a, cudaStream_t st) {
@@ -331,7 +335,8 @@ ittt_status validate_scan(const ittt_scan_problem* p) {
   for (int i = 0; i < 6; ++i)
     if (ld[i] < 0 || (ld[i] && ld[i] < (i < 4 ? p->d : gn))) return ITTT_ERR_INVALID_ARG;
   if (p->d % p->G != 0) return ITTT_ERR_INVALID_ARG;
-  if (p->N > 256 || p->B >= (1ll << 31) || p->T > (1ll << 30)) return ITTT_ERR_UNSUPPORTED;
+  // the walk over sequences (and the one over tokens) may step past its end in 32 bits
+  if (p->N > 256 || p->B > (1ll << 30) || p->T > (1ll << 30)) return ITTT_ERR_UNSUPPORTED;
   for (int i = 0; i < 6; ++i)
     if (!fits(p->B * p->T, i < 4 ? p->d : gn, ld[i])) return ITTT_ERR_UNSUPPORTED;
   if (p->B * p->d >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
@@ -401,7 +406,8 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   const double elements = double(p->B) * p->d * p->T * double((p->N + 3) / 4 * 4);
   const double serial_us = std::max(2.0 + 0.24 * p->T, 1.4e-6 * elements);
   const double wave = c.passes == 2 ? 11.7 + 0.45 * p->N : 4.0 + 0.42 * p->N;
-  const double chunk_us = std::max(c.passes == 2 ? 13.0 : 7.5, double(groups) * cdiv(p->T, kScanChunk) / workers * wave);
+  const double chunk_us = std::max(c.passes == 2 ? 13.0 : 7.5,
+                                   double(groups) * cdiv(p->T, kScanChunk) / workers * wave);
   c.short_call = p->T == 1 || serial_us < chunk_us;
   if (c.short_call) return c;
   const long long chunks = cdiv(p->T, kScanChunk);
@@ -415,7 +421,8 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   bool split = false;
   for (long long rc = 1; rc < chunks; rc += std::max(1ll, rc / 8)) {
     const long long tasks = groups * cdiv(chunks, rc);
-    const double cost = 1.6 * (double(rc) + 0.5) * double(cdiv(tasks, workers)) * chunk_time(double(tasks)) + 4.0;
+    const double cost =
+        1.6 * (double(rc) + 0.5) * double(cdiv(tasks, workers)) * chunk_time(double(tasks)) + 4.0;
     if (cost < best) {
       best = cost;
       run_chunks = rc;
@@ -463,8 +470,8 @@ ittt_status scan_short_sized(const ScanArgs<T_>& a, int sms, cudaStream_t st) {
     // 5120 x 16: 12.9 us, 13.2 with eight, 14.0 with six or with all sequences at once)
     const long long x = cdiv(threads, 128);
     const long long y = std::max(1ll, std::min<long long>(a.B, 10ll * sms / x));
-    return launch_pdl(scan_token_kernel<T_, VEC>, dim3(unsigned(x), unsigned(std::min(y, 65535ll))), dim3(128), st, a,
-                      lanes);
+    return launch_pdl(scan_token_kernel<T_, VEC>, dim3(unsigned(x), unsigned(std::min(y, 65535ll))),
+                      dim3(128), st, a, lanes);
   }
   if (npl == 4) return launch(scan_serial_kernel<T_, 4, VEC>, a.B);
   return launch(scan_serial_kernel<T_, 8, VEC>, a.B);
@@ -481,12 +488,13 @@ ittt_status scan_short(const ScanArgs<T_>& a, int sms, cudaStream_t st) {
 
 template <typename T_, int P, bool STATE_ONLY>
 ittt_status scan_chunks_wide(const ScanArgs<T_>& a, const ScanPlan& pl, long long tasks, int sms,
-                        cudaStream_t st) {
+                             cudaStream_t st) {
   static std::atomic<bool> granted[kMaxDevices] = {};
   auto kern = scan_chunk_kernel<T_, P, STATE_ONLY>;
   if (!grant_smem(kern, scan_smem_bytes<T_, P>(256), granted)) return ITTT_ERR_CUDA;
-  return launch_clusters(kern, unsigned(std::min<long long>(tasks, (long long)ScanShape<T_, P>::CTAS * sms)), 1, kScanThreads,
-                         scan_smem_bytes<T_, P>(a.N), st, a, pl, g_wait_ns.load());
+  const long long grid = std::min<long long>(tasks, (long long)ScanShape<T_, P>::CTAS * sms);
+  return launch_clusters(kern, unsigned(grid), 1, kScanThreads, scan_smem_bytes<T_, P>(a.N), st, a, pl,
+                         g_wait_ns.load());
 }
 
 template <typename T_, bool STATE_ONLY>
@@ -564,7 +572,10 @@ ittt_status ittt_causal_conv(const ittt_conv_problem* p, const void* X, const vo
   const NvtxRange nvtx_range("ittt_causal_conv");
   ittt_status s = validate_conv(p);
   if (s != ITTT_OK) return s;
-  if (!X || !conv_kernel || !Y || X == Y || Y == state_in || Y == state_out) return ITTT_ERR_INVALID_ARG;
+  if (!X || !conv_kernel || !Y || X == Y || Y == state_in || Y == state_out || Y == conv_kernel || Y == bias)
+    return ITTT_ERR_INVALID_ARG;
+  if (state_out && p->k > 1 && (state_out == X || state_out == conv_kernel || state_out == bias))
+    return ITTT_ERR_INVALID_ARG;
   const size_t es = p->dtype == ITTT_BF16 ? 2 : 4;
   const long long rows = p->B * p->T;
   const size_t state = size_t(p->B) * size_t(p->k - 1) * p->d * es;
@@ -602,8 +613,10 @@ ittt_status ittt_selective_scan(const ittt_scan_problem* p, const void* U, const
   ittt_status s = validate_scan(p);
   if (s != ITTT_OK) return s;
   if (!U || !delta || !A || !Bm || !Cm || !Y) return ITTT_ERR_INVALID_ARG;
-  if (Y == U || Y == delta || Y == Z || Y == Bm || Y == Cm || Y == state_in || Y == state_out)
-    return ITTT_ERR_INVALID_ARG;
+  if (Y == state_in || Y == state_out) return ITTT_ERR_INVALID_ARG;
+  for (const void* in : {U, delta, Z, Bm, Cm, static_cast<const void*>(A), static_cast<const void*>(D),
+                         static_cast<const void*>(dt_bias)})
+    if (in && (Y == in || state_out == in)) return ITTT_ERR_INVALID_ARG;
   const size_t es = p->dtype == ITTT_BF16 ? 2 : 4;
   const long long rows = p->B * p->T, gn = (long long)p->G * p->N;
   const size_t state = size_t(p->B) * p->d * p->N * 4;

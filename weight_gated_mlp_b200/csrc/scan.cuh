@@ -6,19 +6,26 @@
 // computes it takes 16 a clock and SM), so no kernel computes one twice.
 //
 //   scan_token_kernel   single tokens: lanes over the state, sequence after sequence.
-//       Bound by the state's bytes.
+//       Bound by the state's bytes (64 sequences of 5120 x 16: 12.9 us, 6.9 us at HBM's
+//       copy rate).
 //   scan_serial_kernel  short calls: lanes over the state, four or eight elements a
-//       lane, four tokens at a time.
-//   scan_chunk_kernel   prompts: 8 channels a CTA, 256 tokens at a time.  A
-//       thread owns two neighbouring channels and 8 consecutive tokens, a warp two
-//       channels and the whole chunk.  For four state elements at once a thread runs
-//       the recurrence of its tokens from zero into y, and keeps for each token
-//       g = C times the decay since the span's start; the warp joins its 32 spans (a
-//       span's decay is exp(A sum s): one exponential and one rounding for 8
+//       lane, four tokens at a time.  Bound by the latency of one token after the other
+//       (0.24 us each), or by the exponentials where there are many sequences.
+//   scan_chunk_kernel   prompts: 256 tokens at a time.  A thread owns two neighbouring
+//       channels and 8 consecutive tokens, a warp two channels and the whole chunk, a
+//       CTA one or two such pairs of channels a warp.  For four state elements at once a
+//       thread runs the recurrence of its tokens from zero into y, and keeps for each
+//       token g = C times the decay since the span's start; the warp joins its 32 spans
+//       (a span's decay is exp(A sum s): one exponential and one rounding for 8
 //       tokens); then y += g h with the span's true start h.  Two channels a thread halve
 //       what a state element costs in shared-memory reads of B and C (32 words a
 //       clock and SM, however many lanes read the same word), and the joins stay
 //       inside a warp, so the CTA meets four times a chunk only.
+//       8192 x 5120 x 16 in bf16: 480 us, where the exponentials alone need 150 us and
+//       the bytes 51 us.  About 15 instructions an element go out in 56% of the issue
+//       slots; the exponentials' unit is 40% busy.  What remains is latency: a warp's
+//       join is a chain of shuffles, and three CTAs an SM (the registers' limit) do
+//       not cover it.
 #pragma once
 
 #include "common.cuh"
@@ -294,22 +301,23 @@ __global__ void __launch_bounds__(128) scan_token_kernel(const ScanArgs<T_> a, i
 
 // ---------------------------------------------------------------- prompts
 
-// Four warps, two pairs at once, and in bf16 168 registers a thread and three CTAs an
-// SM: 470 us for 8192 x 5120 x 16.  One pair at once 491 us, with 128 registers and
-// four CTAs 534 us (584 us with two pairs, which then spill), eight warps and 128
-// registers 514 us, 255 registers and two CTAs 532 us, spans of four tokens 517 us.
-// fp32 holds twice the values of B and C and wants the registers: 80 us with two CTAs
-// for 1667 tokens x 1000 x 32, 105 us with three.
+// Four warps, two pairs of state elements at once, and in bf16 168 registers a thread
+// and three CTAs an SM.  8192 x 5120 x 16, one pass, each against 470 us in the build it
+// was tried in: one pair at once 491 us, with 128 registers and four CTAs 534 us (584 us
+// with two pairs, which then spill), eight warps and 128 registers 514 us, 255 registers
+// and two CTAs 532 us, spans of four tokens 517 us.  fp32 holds twice the values of B and
+// C and wants the registers: 81 us with two CTAs for 1667 tokens x 1000 x 32, 105 us with
+// three.
 constexpr int kScanWarps = 4;
 constexpr int kScanThreads = 32 * kScanWarps;
 // Channels a CTA: a warp takes P pairs of channels one after the other.  Two halve
 // what staging B and C costs a channel (8 x 1024 x 5120 x 16: 436 us, 474 with one);
-// one makes twice as many tasks (1 x 8192 x 5120: 470 us, 543 with two, whose 320
+// one makes twice as many tasks (1 x 8192 x 5120: 480 us, 543 with two, whose 320
 // channel blocks leave CTAs without work).
 __host__ __device__ constexpr int scan_ch(int P) { return 2 * kScanWarps * P; }
-constexpr int kScanK = 8;                         // tokens a span, one span a lane
-constexpr int kScanChunk = 32 * kScanK;           // tokens a chunk
-constexpr int kScanJ = 2;                    // pairs of state elements at once
+constexpr int kScanK = 8;                // tokens a span, one span a lane
+constexpr int kScanChunk = 32 * kScanK;  // tokens a chunk
+constexpr int kScanJ = 2;                // pairs of state elements at once
 
 // How the work of a call is cut.  A task is one channel block of one sequence
 // over one run of tokens; tasks are handed out run by run.
@@ -591,7 +599,8 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
       const long long row = row0 + t0, gn = (long long)g * a.N;
       fetch_slab<T_, P>(raw, a.Bm + row * a.ldb + gn, a.ldb, tokens, a.N, n0, pieces_b);
       if (!STATE_ONLY)
-        fetch_slab<T_, P>(raw + kScanChunk * S::SLAB, a.Cm + row * a.ldc + gn, a.ldc, tokens, a.N, n0, pieces_c);
+        fetch_slab<T_, P>(raw + kScanChunk * S::SLAB, a.Cm + row * a.ldc + gn, a.ldc, tokens, a.N, n0,
+                          pieces_c);
     };
     if (t_begin < t_end) {
       fetch_inputs(t_begin);
@@ -643,195 +652,196 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
 
 #pragma unroll 1
       for (int pass = 0; pass < P; ++pass) {
-      // this thread's two channels (past nch: zeros in, nothing out)
-      const int ch = 2 * (warp + kScanWarps * pass);
-      const T_* my_rows = rows + lane * S::ROW_SPAN + ch;
-      float* join_state = state + ch * NP + join_at;
-      const float* join_A2 = A2s + ch * NP + join_at;
-      const bool last_pass = pass == P - 1;
+        // this thread's two channels (past nch: zeros in, nothing out)
+        const int ch = 2 * (warp + kScanWarps * pass);
+        const T_* my_rows = rows + lane * S::ROW_SPAN + ch;
+        float* join_state = state + ch * NP + join_at;
+        const float* join_A2 = A2s + ch * NP + join_at;
+        const bool last_pass = pass == P - 1;
 #pragma unroll 1
-      for (int n0 = 0; n0 < NP; n0 += S::SLAB) {
-        const bool fresh = pass == 0 || !one_slab;  // else B and C are laid out already
-        if (fresh) {
-          copy_wait<0>();
-          __syncthreads();  // the copies are in; the tiles' readers of the step before are done
-        }
-        if (n0 == 0) {
-          if (!STATE_ONLY && a.Z && pass == 0) {
-            fetch_rows<T_, P>(rows + 2 * S::ROW_TILE, a.Z + (row0 + t0) * a.ldz + c0, a.ldz, tokens, nch, pieces_z);
-            copy_commit();
+        for (int n0 = 0; n0 < NP; n0 += S::SLAB) {
+          const bool fresh = pass == 0 || !one_slab;  // else B and C are laid out already
+          if (fresh) {
+            copy_wait<0>();
+            __syncthreads();  // the copies are in; the tiles' readers of the step before are done
           }
-          const float2 bias = *reinterpret_cast<const float2*>(biases + ch);
-          const float2 skip = *reinterpret_cast<const float2*>(skips + ch);
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int k = 0; k < kScanK; ++k) {
-            const float2 u = load_two(my_rows + k * S::CH);
-            float2 s = load_two(my_rows + S::ROW_TILE + k * S::CH);
-            s.x += bias.x;
-            s.y += bias.y;
-            if (a.softplus) {
-              s.x = softplus_f32(s.x);
-              s.y = softplus_f32(s.y);
+          if (n0 == 0) {
+            if (!STATE_ONLY && a.Z && pass == 0) {
+              fetch_rows<T_, P>(rows + 2 * S::ROW_TILE, a.Z + (row0 + t0) * a.ldz + c0, a.ldz, tokens, nch,
+                                pieces_z);
+              copy_commit();
             }
-            if (mine0 + k >= tokens) s = make_float2(0.f, 0.f);  // behind the end: the state passes
-            sum.x += s.x;
-            sum.y += s.y;
-            s2[k] = pack2(s.x, s.y);
-            su[k] = make_float2(s.x * u.x, s.y * u.y);
-            // no 0 * inf where there is no skip
-            y2[k] = a.D ? pack2(skip.x * u.x, skip.y * u.y) : pack2(0.f, 0.f);
-          }
-#pragma unroll
-          for (int i = 0; i < kJoinSpans; ++i) {
-            const float x = __shfl_sync(0xffffffffu, sum.x, first_span + i);
-            const float z = __shfl_sync(0xffffffffu, sum.y, first_span + i);
-            join_sum[i] = (q & 1) ? z : x;
-          }
-          if constexpr (STATE_ONLY) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
-              sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
-            }
-            if (lane == 0) {
-              totals[ch] += sum.x;
-              totals[ch + 1] += sum.y;
-            }
-          }
-        }
-        if (fresh) {
-          lay_out<T_, P>(tiles, raw);
-          if (!STATE_ONLY) lay_out<T_, P>(tiles + S::PAIRS * S::PAIR_TILE, raw + kScanChunk * S::SLAB);
-        }
-        // before the tiles are read, and before the rows, read above by all, are replaced
-        if (fresh || last_pass) __syncthreads();
-        // what comes next arrives during the recurrences
-        if (n0 + S::SLAB < NP) {
-          fetch_bc(t0, n0 + S::SLAB);
-        } else if (!last_pass) {
-          if (!one_slab) fetch_bc(t0, 0);
-        } else if (t0 + kScanChunk < t_end) {
-          fetch_inputs(t0 + kScanChunk);
-          fetch_bc(t0 + kScanChunk, 0);
-        }
-        copy_commit();
-
-        const int pairs = min(S::PAIRS, (NP - n0) >> 1);
-#pragma unroll 1
-        for (int p = 0; p < pairs; p += kScanJ) {
-          const int n = n0 + 2 * p;
-          // the recurrence from zero, its outputs, and g = C times the decay since the
-          // span's start, which the start state is multiplied with once it is known
-          f32x2 g[kScanJ][2][kScanK], h[kScanJ][2];
-#pragma unroll
-          for (int j = 0; j < kScanJ; ++j) {
-            const uint32_t* bp = tiles + (p + j) * S::PAIR_TILE + lane * S::PAIR_SPAN;
-            const float2 Ax = *reinterpret_cast<const float2*>(A2s + ch * NP + n + 2 * j);
-            const float2 Ay = *reinterpret_cast<const float2*>(A2s + (ch + 1) * NP + n + 2 * j);
-            const f32x2 A0 = pack2(Ax.x, Ay.x), A1 = pack2(Ax.y, Ay.y);
-            const PairSpan<T_> B(bp), C(bp + S::PAIRS * S::PAIR_TILE);
-            f32x2 h0 = 0ull, h1 = 0ull, p0 = 0ull, p1 = 0ull;
+            const float2 bias = *reinterpret_cast<const float2*>(biases + ch);
+            const float2 skip = *reinterpret_cast<const float2*>(skips + ch);
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kScanK; ++k) {
-              float x, z;
-              unpack2(mul2(s2[k], A0), x, z);
-              const f32x2 a0 = pack2(exp2_approx(x), exp2_approx(z));
-              unpack2(mul2(s2[k], A1), x, z);
-              const f32x2 a1 = pack2(exp2_approx(x), exp2_approx(z));
-              h0 = fma2(a0, h0, pack2(su[k].x * B.lo(k), su[k].y * B.lo(k)));
-              h1 = fma2(a1, h1, pack2(su[k].x * B.hi(k), su[k].y * B.hi(k)));
-              if (!STATE_ONLY) {
-                p0 = k ? mul2(p0, a0) : a0;
-                p1 = k ? mul2(p1, a1) : a1;
-                float y0, y1;
-                unpack2(y2[k], y0, y1);
-                unpack2(h0, x, z);
-                y0 = fmaf(x, C.lo(k), y0);
-                y1 = fmaf(z, C.lo(k), y1);
-                unpack2(h1, x, z);
-                y2[k] = pack2(fmaf(x, C.hi(k), y0), fmaf(z, C.hi(k), y1));
-                unpack2(p0, x, z);
-                g[j][0][k] = pack2(x * C.lo(k), z * C.lo(k));
-                unpack2(p1, x, z);
-                g[j][1][k] = pack2(x * C.hi(k), z * C.hi(k));
+              const float2 u = load_two(my_rows + k * S::CH);
+              float2 s = load_two(my_rows + S::ROW_TILE + k * S::CH);
+              s.x += bias.x;
+              s.y += bias.y;
+              if (a.softplus) {
+                s.x = softplus_f32(s.x);
+                s.y = softplus_f32(s.y);
               }
+              if (mine0 + k >= tokens) s = make_float2(0.f, 0.f);  // behind the end: the state passes
+              sum.x += s.x;
+              sum.y += s.y;
+              s2[k] = pack2(s.x, s.y);
+              su[k] = make_float2(s.x * u.x, s.y * u.y);
+              // no 0 * inf where there is no skip
+              y2[k] = a.D ? pack2(skip.x * u.x, skip.y * u.y) : pack2(0.f, 0.f);
             }
-            h[j][0] = h0;
-            h[j][1] = h1;
-          }
-          // join the warp's spans
-          __syncwarp();  // the starts of the pairs before have been read
-#pragma unroll
-          for (int j = 0; j < kScanJ; ++j)
-            *reinterpret_cast<ulonglong2*>(my_end + 4 * j) = make_ulonglong2(h[j][0], h[j][1]);
-          __syncwarp();
-          {
-            const float A2 = join_A2[n], h_in = join_state[n];
-            float e[kJoinSpans], d[kJoinSpans];
 #pragma unroll
             for (int i = 0; i < kJoinSpans; ++i) {
-              e[i] = join_ends[i * kEndsSpan];
-              d[i] = exp2_approx(join_sum[i] * A2);
+              const float x = __shfl_sync(0xffffffffu, sum.x, first_span + i);
+              const float z = __shfl_sync(0xffffffffu, sum.y, first_span + i);
+              join_sum[i] = (q & 1) ? z : x;
             }
-            // this lane's spans as one: E + D h
-            float E = e[0], D = d[0];
+            if constexpr (STATE_ONLY) {
 #pragma unroll
-            for (int i = 1; i < kJoinSpans; ++i) {
-              E = fmaf(d[i], E, e[i]);
-              D *= d[i];
-            }
-            // and the lanes before it
-#pragma unroll
-            for (int o = kEndsSpan; o < 32; o <<= 1) {
-              const float Eo = __shfl_up_sync(0xffffffffu, E, o), Do = __shfl_up_sync(0xffffffffu, D, o);
-              if (lane >= o) {
-                E = fmaf(D, Eo, E);
-                D *= Do;
+              for (int o = 16; o > 0; o >>= 1) {
+                sum.x += __shfl_xor_sync(0xffffffffu, sum.x, o);
+                sum.y += __shfl_xor_sync(0xffffffffu, sum.y, o);
+              }
+              if (lane == 0) {
+                totals[ch] += sum.x;
+                totals[ch + 1] += sum.y;
               }
             }
-            if (lane >= 32 - kEndsSpan) join_state[n] = fmaf(D, h_in, E);
-            if (!STATE_ONLY) {
-              const float Eo = __shfl_up_sync(0xffffffffu, E, kEndsSpan);
-              const float Do = __shfl_up_sync(0xffffffffu, D, kEndsSpan);
-              float start = lane >= kEndsSpan ? fmaf(Do, h_in, Eo) : h_in;
+          }
+          if (fresh) {
+            lay_out<T_, P>(tiles, raw);
+            if (!STATE_ONLY) lay_out<T_, P>(tiles + S::PAIRS * S::PAIR_TILE, raw + kScanChunk * S::SLAB);
+          }
+          // before the tiles are read, and before the rows, read above by all, are replaced
+          if (fresh || last_pass) __syncthreads();
+          // what comes next arrives during the recurrences
+          if (n0 + S::SLAB < NP) {
+            fetch_bc(t0, n0 + S::SLAB);
+          } else if (!last_pass) {
+            if (!one_slab) fetch_bc(t0, 0);
+          } else if (t0 + kScanChunk < t_end) {
+            fetch_inputs(t0 + kScanChunk);
+            fetch_bc(t0 + kScanChunk, 0);
+          }
+          copy_commit();
+
+          const int pairs = min(S::PAIRS, (NP - n0) >> 1);
+#pragma unroll 1
+          for (int p = 0; p < pairs; p += kScanJ) {
+            const int n = n0 + 2 * p;
+            // the recurrence from zero, its outputs, and g = C times the decay since the
+            // span's start, which the start state is multiplied with once it is known
+            f32x2 g[kScanJ][2][kScanK], h[kScanJ][2];
+#pragma unroll
+            for (int j = 0; j < kScanJ; ++j) {
+              const uint32_t* bp = tiles + (p + j) * S::PAIR_TILE + lane * S::PAIR_SPAN;
+              const float2 Ax = *reinterpret_cast<const float2*>(A2s + ch * NP + n + 2 * j);
+              const float2 Ay = *reinterpret_cast<const float2*>(A2s + (ch + 1) * NP + n + 2 * j);
+              const f32x2 A0 = pack2(Ax.x, Ay.x), A1 = pack2(Ax.y, Ay.y);
+              const PairSpan<T_> B(bp), C(bp + S::PAIRS * S::PAIR_TILE);
+              f32x2 h0 = 0ull, h1 = 0ull, p0 = 0ull, p1 = 0ull;
+#pragma unroll
+              for (int k = 0; k < kScanK; ++k) {
+                float x, z;
+                unpack2(mul2(s2[k], A0), x, z);
+                const f32x2 a0 = pack2(exp2_approx(x), exp2_approx(z));
+                unpack2(mul2(s2[k], A1), x, z);
+                const f32x2 a1 = pack2(exp2_approx(x), exp2_approx(z));
+                h0 = fma2(a0, h0, pack2(su[k].x * B.lo(k), su[k].y * B.lo(k)));
+                h1 = fma2(a1, h1, pack2(su[k].x * B.hi(k), su[k].y * B.hi(k)));
+                if (!STATE_ONLY) {
+                  p0 = k ? mul2(p0, a0) : a0;
+                  p1 = k ? mul2(p1, a1) : a1;
+                  float y0, y1;
+                  unpack2(y2[k], y0, y1);
+                  unpack2(h0, x, z);
+                  y0 = fmaf(x, C.lo(k), y0);
+                  y1 = fmaf(z, C.lo(k), y1);
+                  unpack2(h1, x, z);
+                  y2[k] = pack2(fmaf(x, C.hi(k), y0), fmaf(z, C.hi(k), y1));
+                  unpack2(p0, x, z);
+                  g[j][0][k] = pack2(x * C.lo(k), z * C.lo(k));
+                  unpack2(p1, x, z);
+                  g[j][1][k] = pack2(x * C.hi(k), z * C.hi(k));
+                }
+              }
+              h[j][0] = h0;
+              h[j][1] = h1;
+            }
+            // join the warp's spans
+            __syncwarp();  // the starts of the pairs before have been read
+#pragma unroll
+            for (int j = 0; j < kScanJ; ++j)
+              *reinterpret_cast<ulonglong2*>(my_end + 4 * j) = make_ulonglong2(h[j][0], h[j][1]);
+            __syncwarp();
+            {
+              const float A2 = join_A2[n], h_in = join_state[n];
+              float e[kJoinSpans], d[kJoinSpans];
 #pragma unroll
               for (int i = 0; i < kJoinSpans; ++i) {
-                join_ends[i * kEndsSpan] = start;
-                start = fmaf(d[i], start, e[i]);
+                e[i] = join_ends[i * kEndsSpan];
+                d[i] = exp2_approx(join_sum[i] * A2);
+              }
+              // this lane's spans as one: E + D h
+              float E = e[0], D = d[0];
+#pragma unroll
+              for (int i = 1; i < kJoinSpans; ++i) {
+                E = fmaf(d[i], E, e[i]);
+                D *= d[i];
+              }
+              // and the lanes before it
+#pragma unroll
+              for (int o = kEndsSpan; o < 32; o <<= 1) {
+                const float Eo = __shfl_up_sync(0xffffffffu, E, o), Do = __shfl_up_sync(0xffffffffu, D, o);
+                if (lane >= o) {
+                  E = fmaf(D, Eo, E);
+                  D *= Do;
+                }
+              }
+              if (lane >= 32 - kEndsSpan) join_state[n] = fmaf(D, h_in, E);
+              if (!STATE_ONLY) {
+                const float Eo = __shfl_up_sync(0xffffffffu, E, kEndsSpan);
+                const float Do = __shfl_up_sync(0xffffffffu, D, kEndsSpan);
+                float start = lane >= kEndsSpan ? fmaf(Do, h_in, Eo) : h_in;
+#pragma unroll
+                for (int i = 0; i < kJoinSpans; ++i) {
+                  join_ends[i * kEndsSpan] = start;
+                  start = fmaf(d[i], start, e[i]);
+                }
               }
             }
-          }
-          if (STATE_ONLY) continue;
-          __syncwarp();
+            if (STATE_ONLY) continue;
+            __syncwarp();
 #pragma unroll
-          for (int j = 0; j < kScanJ; ++j) {
-            const ulonglong2 start = *reinterpret_cast<const ulonglong2*>(my_end + 4 * j);
+            for (int j = 0; j < kScanJ; ++j) {
+              const ulonglong2 start = *reinterpret_cast<const ulonglong2*>(my_end + 4 * j);
 #pragma unroll
-            for (int k = 0; k < kScanK; ++k)
-              y2[k] = fma2(g[j][1][k], start.y, fma2(g[j][0][k], start.x, y2[k]));
+              for (int k = 0; k < kScanK; ++k)
+                y2[k] = fma2(g[j][1][k], start.y, fma2(g[j][0][k], start.x, y2[k]));
+            }
           }
         }
-      }
 
-      if (!STATE_ONLY) {
-        if (pass == 0) {
-          copy_wait<1>();   // Z is in (the next step's copies may still run)
-          __syncthreads();
-        }
-        T_* zy = const_cast<T_*>(my_rows) + 2 * S::ROW_TILE;  // Z's place becomes Y's
-#pragma unroll
-        for (int k = 0; k < kScanK; ++k) {
-          float y0, y1;
-          unpack2(y2[k], y0, y1);
-          if (a.Z) {
-            const float2 z = load_two(zy + k * S::CH);
-            y0 *= silu_fast(z.x);
-            y1 *= silu_fast(z.y);
+        if (!STATE_ONLY) {
+          if (pass == 0) {
+            copy_wait<1>();   // Z is in (the next step's copies may still run)
+            __syncthreads();
           }
-          store_two(zy + k * S::CH, y0, y1);
+          T_* zy = const_cast<T_*>(my_rows) + 2 * S::ROW_TILE;  // Z's place becomes Y's
+#pragma unroll
+          for (int k = 0; k < kScanK; ++k) {
+            float y0, y1;
+            unpack2(y2[k], y0, y1);
+            if (a.Z) {
+              const float2 z = load_two(zy + k * S::CH);
+              y0 *= silu_fast(z.x);
+              y1 *= silu_fast(z.y);
+            }
+            store_two(zy + k * S::CH, y0, y1);
+          }
         }
-      }
       }
       if (!STATE_ONLY) {
         __syncthreads();
