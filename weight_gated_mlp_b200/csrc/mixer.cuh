@@ -31,12 +31,15 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// x / (1 + e^-x) by the hardware's quotient (2 ulp).  Below -126 the value is under
+// x / (1 + e^-x) by the hardware's reciprocal (2 ulp).  The reciprocal of a denominator
+// above 2^126 is 0 (the value is under 2^-119).  Below -126 the value is under
 // 2^-174, and the quotient by an infinite denominator gives the 0 it rounds to; the
 // argument is held there so that -inf gives 0 too (NaN stays NaN).
 __device__ __forceinline__ float silu_fast(float x) {
   asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x));
-  return __fdividef(x, 1.f + exp2_approx(-kLog2e * x));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + exp2_approx(-kLog2e * x)));
+  return x * r;
 }
 
 // act(x) in fp32; at -inf the limit (0 for all but the identity).  A template
@@ -67,6 +70,41 @@ __device__ __noinline__ float activate_any(float x, int act) {
   }
 }
 
+// Two fp32 values in one 64-bit register and the paired instructions on them
+// (one issue slot for two products).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Two neighbouring channels of a row.
+__device__ __forceinline__ float2 load_two(const __nv_bfloat16* p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 load_two(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ void store_two(__nv_bfloat16* p, float x, float y) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
+}
+__device__ __forceinline__ void store_two(float* p, float x, float y) {
+  *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
+
 // ------------------------------------------------------------------ linear
 
 template <typename T_>
@@ -93,8 +131,9 @@ __device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, in
 }
 
 // Bound by reading X and writing Y once, with the activation's two special-function
-// results a value close behind: 8192 x 5120 in bf16 with four taps and silu 37.3 us, 4.5
-// TB/s (torch's copy of the same bytes 27.2 us).  A thread owns V neighbouring channels (16 bytes; 1
+// results a value close behind: 8192 x 5120 in bf16 with four taps and silu 35.2 us, 4.8
+// TB/s (torch's copy of the same bytes 27.2 us; 37.3 us with one channel an instruction
+// and eight steps a thread).  A thread owns V neighbouring channels (16 bytes; 1
 // where widths or alignment do not allow that) over `steps` times four tokens.  It
 // holds the KT - 1 rows before and four more, and asks for the next four before it
 // computes, so that loads and arithmetic overlap; a thread's first KT - 1 rows are
@@ -132,7 +171,9 @@ __global__ void __launch_bounds__(128, V > 1 && KT <= 4 ? 4 : 1)
       next[i] = t0 + i < t_end ? *reinterpret_cast<const Row*>(xp + i * a.ldx) : Row{};
 #pragma unroll
     for (int i = 0; i < KT - 1; ++i) rows[R + i] = before(t0 + i - (KT - 1));
-    float w[KT][V], bias[V];
+    float bias[V];
+    float w1[KT];                 // V == 1
+    f32x2 w2[KT][(V + 1) / 2];    // V > 1
     {
       // the taps of V channels are V * KT contiguous elements
       const Row* wp = reinterpret_cast<const Row*>(a.w + (long long)c * KT);
@@ -140,9 +181,12 @@ __global__ void __launch_bounds__(128, V > 1 && KT <= 4 ? 4 : 1)
 #pragma unroll
       for (int i = 0; i < KT; ++i) *reinterpret_cast<Row*>(taps + i * V) = __ldg(wp + i);
 #pragma unroll
-      for (int j = 0; j < KT; ++j)
+      for (int j = 0; j < KT; ++j) {
+        w1[j] = to_f32(taps[j]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) w[j][i] = to_f32(taps[i * KT + j]);
+        for (int i = 0; i + 1 < V; i += 2)
+          w2[j][i / 2] = pack2(to_f32(taps[i * KT + j]), to_f32(taps[(i + 1) * KT + j]));
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) bias[i] = a.bias ? to_f32(a.bias[c + i]) : 0.f;
     }
@@ -161,13 +205,23 @@ __global__ void __launch_bounds__(128, V > 1 && KT <= 4 ? 4 : 1)
       for (int r = 0; r < R; ++r) {
         if (t + r < t_end) {
           float y[V];
+          if (V == 1) {
+            y[0] = bias[0];
 #pragma unroll
-          for (int i = 0; i < V; ++i) y[i] = bias[i];
+            for (int j = 0; j < KT; ++j)
+              y[0] = fmaf(w1[j], to_f32(*reinterpret_cast<const T_*>(&rows[r + j])), y[0]);
+          } else {
+            // two channels an instruction
 #pragma unroll
-          for (int j = 0; j < KT; ++j) {
-            const T_* x = reinterpret_cast<const T_*>(&rows[r + j]);
+            for (int i = 0; i + 1 < V; i += 2) {
+              f32x2 acc = pack2(bias[i], bias[i + 1]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) y[i] = fmaf(w[j][i], to_f32(x[i]), y[i]);
+              for (int j = 0; j < KT; ++j) {
+                const float2 x = load_two(reinterpret_cast<const T_*>(&rows[r + j]) + i);
+                acc = fma2(w2[j][i / 2], pack2(x.x, x.y), acc);
+              }
+              unpack2(acc, y[i], y[i + 1]);
+            }
           }
           Row out;
           T_* o = reinterpret_cast<T_*>(&out);
@@ -178,8 +232,9 @@ __global__ void __launch_bounds__(128, V > 1 && KT <= 4 ? 4 : 1)
 #pragma unroll
             for (int i = 0; i < V; ++i) y[i] = activate_any(y[i], a.act);
           }
+          if (V == 1) o[0] = from_f32<T_>(y[0]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = from_f32<T_>(y[i]);
+          for (int i = 0; i + 1 < V; i += 2) store_two(o + i, y[i], y[i + 1]);
           *reinterpret_cast<Row*>(Y + r * a.ldy) = out;
         }
       }

@@ -259,7 +259,23 @@ ittt_status validate_conv(const ittt_conv_problem* p) {
   return ITTT_OK;
 }
 
-// Steps of four tokens a thread: 8 while that leaves every SM 16 warps, down to 2.
+// CTAs of a kernel without dynamic shared memory that an SM of the current device holds
+// (0: the device does not say).
+template <typename Kern>
+int resident_ctas(Kern kern, int threads, std::atomic<int>* known) {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, 0) != cudaSuccess) return 0;
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Steps of four tokens a thread: 8 while that leaves every SM 16 warps, down to 2.  More
+// CTAs than the GPU holds at once: the number from 6 to 18 that wastes least of the last
+// wave (a thread's start counts as one step): 8192 x 5120 takes 35.2 us in one wave of 18
+// steps and 35.1 us in two of 9, but 36.4 us in 8 steps, whose third wave is a sixth
+// full, and 40.4 us in 16.
 template <typename T_, int V, int KT, int ACT>
 ittt_status causal_conv_vec(const CausalConvArgs<T_>& a, cudaStream_t st) {
   const int sms = num_sms();
@@ -267,10 +283,22 @@ ittt_status causal_conv_vec(const CausalConvArgs<T_>& a, cudaStream_t st) {
   const long long groups = a.d / V;
   int steps = 8;
   while (steps > 2 && a.B * cdiv(a.T, 4 * steps) * groups < 512ll * sms) steps /= 2;
+  auto kern = causal_conv_vec_kernel<T_, V, KT, ACT>;
+  static std::atomic<int> known[kMaxDevices] = {};
+  const long long slots = (long long)resident_ctas(kern, 128, known) * sms;
+  if (slots <= 0) return ITTT_ERR_CUDA;
+  auto ctas = [&](int n) { return cdiv(a.B * cdiv(a.T, 4 * n) * groups, 128); };
+  if (ctas(steps) > slots) {
+    long long best = 0;
+    for (int n = 6; n <= 18; ++n) {
+      const long long cost = cdiv(ctas(n), slots) * (n + 1);
+      if (n == 6 || cost < best) best = cost, steps = n;
+    }
+  }
   const long long runs = cdiv(a.T, 4 * steps), total = a.B * runs * groups;
   if (total >= (1ll << 32) - 128) return ITTT_ERR_UNSUPPORTED;
-  return launch_pdl(causal_conv_vec_kernel<T_, V, KT, ACT>, dim3(unsigned(cdiv(total, 128))), dim3(128),
-                    st, a, unsigned(total), unsigned(groups), unsigned(runs), steps);
+  return launch_pdl(kern, dim3(unsigned(cdiv(total, 128))), dim3(128), st, a, unsigned(total),
+                    unsigned(groups), unsigned(runs), steps);
 }
 
 template <typename T_, int V, int KT>

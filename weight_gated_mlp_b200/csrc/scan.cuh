@@ -63,28 +63,6 @@ __device__ __forceinline__ float softplus_f32(float x) {
   return fmaf(q, e, x != x ? x : fmaxf(x, 0.f));
 }
 
-// Two fp32 values in one 64-bit register and the paired instructions on them
-// (one issue slot for two products).
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pack2(float x, float y) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-  return r;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float& x, float& y) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // ------------------------------------------------------------ short calls
 
 // Four neighbouring values as they are in memory.  The short kernels issue every
@@ -505,19 +483,6 @@ struct PairSpan<float> {
   __device__ __forceinline__ float lo(int k) const { return w[2 * k]; }
   __device__ __forceinline__ float hi(int k) const { return w[2 * k + 1]; }
 };
-
-// Two neighbouring channels of a row.
-__device__ __forceinline__ float2 load_two(const __nv_bfloat16* p) {
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ float2 load_two(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ void store_two(__nv_bfloat16* p, float x, float y) {
-  *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
-}
-__device__ __forceinline__ void store_two(float* p, float x, float y) {
-  *reinterpret_cast<float2*>(p) = make_float2(x, y);
-}
 
 // STATE_ONLY: the first of the two passes of a call that is split over time: every
 // run from a zero state, its end state and sum of steps written, no outputs.
