@@ -7,8 +7,11 @@
 //       columns of K in registers while the present ones are multiplied.  The
 //       CTAs of a cluster split K where there are few tiles and join their sums
 //       through distributed shared memory, in rank order.  Bound by the CUDA cores and
-//       the shared-memory reads that feed them: 333 x 1000 x 1001 with bias and gelu
-//       28.3 us (9.0 us at 128 products a clock and SM).
+//       the shared-memory reads that feed them, a word a product: 333 x 1000 x 1001 with
+//       bias and gelu 25.7 us (9.0 us at 128 products a clock and SM), 1154 x 2168 x
+//       2547 309 us (171).  Two products an instruction leave issue slots to the loads
+//       (28.3 and 373 us with one); 8 x 16 outputs a thread, which read less but leave
+//       half the warps, were slower (480 us and more for the second).
 #pragma once
 
 #include "common.cuh"
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(F32Tile<BM, BN, TM, TN>::THREADS)
       d[0] = rb[i].x, d[S::LDN] = rb[i].y, d[2 * S::LDN] = rb[i].z, d[3 * S::LDN] = rb[i].w;
     }
   };
-  float acc[TM][TN] = {};
+  f32x2 acc2[TM][TN / 2] = {};  // two neighbouring columns
   grid_dependency_wait();
   if (s0 < s1) {
     load(s0);
@@ -219,21 +222,30 @@ __global__ void __launch_bounds__(F32Tile<BM, BN, TM, TN>::THREADS)
     const float* Bb = Bs + buf * KT * S::LDN + tx * 4;
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
-      float x[TM], w[TN];
+      float x[TM];
+      f32x2 w[TN / 2];
 #pragma unroll
       for (int i = 0; i < TM; i += 4)
         *reinterpret_cast<float4*>(x + i) = *reinterpret_cast<const float4*>(Ab + k * S::LDM + i * NY);
 #pragma unroll
       for (int j = 0; j < TN; j += 4)
-        *reinterpret_cast<float4*>(w + j) = *reinterpret_cast<const float4*>(Bb + k * S::LDN + j * NX);
+        *reinterpret_cast<ulonglong2*>(w + j / 2) =
+            *reinterpret_cast<const ulonglong2*>(Bb + k * S::LDN + j * NX);
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+      for (int i = 0; i < TM; ++i) {
+        const f32x2 xx = pack2(x[i], x[i]);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(x[i], w[j], acc[i][j]);
+        for (int j = 0; j < TN / 2; ++j) acc2[i][j] = fma2(xx, w[j], acc2[i][j]);
+      }
     }
     if (s + 1 < s1) put(buf ^ 1);
     __syncthreads();
   }
+  float acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN / 2; ++j) unpack2(acc2[i][j], acc[i][2 * j], acc[i][2 * j + 1]);
   auto row_of = [&](int i) { return (i / 4) * 4 * NY + ty * 4 + i % 4; };
   auto col_of = [&](int j) { return (j / 4) * 4 * NX + tx * 4 + j % 4; };
   if (splits == 1) {

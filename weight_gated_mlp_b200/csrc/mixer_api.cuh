@@ -106,19 +106,25 @@ ittt_status linear_tiles_f32(const LinearArgs<float>& a, int splits, cudaStream_
                          F32Tile<BM, BN, TM, TN>::THREADS, 0, st, a, int(m_tiles));
 }
 
-// Up to 8 rows: the kernel that streams W.  128 x 128 tiles when they fill the
-// SMs; else 64 x 64 tiles, K split over clusters while the CTAs stay within six
-// an SM and every CTA keeps at least 64 columns of K.
+// Up to 8 rows: the kernel that streams W.  Else 64 x 64 tiles, K split over clusters
+// while the CTAs stay within six an SM and every CTA keeps at least 64 columns of K, or,
+// so that the last wave is a small part of the whole, within 21 an SM at 128 columns
+// (us, unsplit and split: 333 x 1000 x 1001 63 and 25 in 8; 1154 x 2168 x 2547 338 and 309
+// in 4; 2048 x 2048 x 2048 430 and 372 in 2, 395 in 4; 4096 x 1024 x 2368, 16 tiles an SM,
+// 419 and 425 in 2).  128 x 128 tiles were slower (422, 386 and 465 us for the
+// last three).
 template <int ACT, bool VEC>
 ittt_status linear_f32_sized(const LinearArgs<float>& a, int sms, cudaStream_t st) {
   if (a.M == 1) return linear_gemv<ACT, 1, VEC>(a, st);
   if (a.M == 2) return linear_gemv<ACT, 2, VEC>(a, st);
   if (a.M <= 4) return linear_gemv<ACT, 4, VEC>(a, st);
   if (a.M <= 8) return linear_gemv<ACT, 8, VEC>(a, st);
-  if (cdiv(a.M, 128) * cdiv(a.N, 128) >= sms) return linear_tiles_f32<ACT, 128, 128, 8, 8, VEC>(a, 1, st);
   const long long tiles = cdiv(a.M, 64) * cdiv(a.N, 64);
   int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= 6ll * sms && a.K >= 64 * splits * 2) splits *= 2;
+  auto twice = [&](int ctas, int columns) {
+    return tiles * splits * 2 <= (long long)ctas * sms && a.K / columns >= splits * 2;
+  };
+  while (splits < 8 && (twice(6, 64) || twice(21, 128))) splits *= 2;
   return linear_tiles_f32<ACT, 64, 64, 8, 8, VEC>(a, splits, st);
 }
 
