@@ -55,6 +55,13 @@ def test_product(M, K, N, dtype):
     check(ittt.linear(X, W, b, R, act="silu"), X, W, b, R, "silu", dtype)
 
 
+@pytest.mark.parametrize("M,K,N", [(700, 600, 1300), (700, 601, 1297), (1300, 300, 3301), (1100, 255, 2000)])
+def test_product_f32_many_tiles(M, K, N):
+    """K split over four CTAs, two and one where the tiles alone fill the GPU."""
+    X, W, b, R = make(M, K, N, "f32", seed=6)
+    check(ittt.linear(X, W, b, R, act="silu"), X, W, b, R, "silu", "f32")
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("M,K,N,dtype", [(1, 256, 72, "bf16"), (5, 256, 71, "bf16"),
                                          (40, 256, 100, "bf16"), (300, 256, 520, "bf16"),

@@ -88,6 +88,26 @@ def test_conv_slices(dtype, d):
     assert (big[:, :, :d] == 9.0).all() and (big[:, :, 2 * d:] == 9.0).all()
 
 
+@pytest.mark.parametrize("B,T,d,part,dtype,lengths", [
+    (2, 5003, 4104, 72, "bf16", None), (3, 4001, 2560, 64, "bf16", [4001, 0, 2999]),
+    (8, 3001, 1001, 11, "f32", None), (2, 4099, 2052, 108, "f32", [4098, 17])])
+def test_conv_more_than_the_gpu_holds(B, T, d, part, dtype, lengths):
+    """Many tokens and channels: the bits of calls on a part of the channels, which are cut
+    otherwise, and the oracle's values at the first ones."""
+    X, w, b, s = conv_inputs(B, T, d, 4, dtype, seed=9)
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    Y, last = ittt.causal_conv(X, w, b, act="silu", state=s, lengths=n)
+    for c in (0, (d // part // 2) * part, d - part):
+        at = slice(c, c + part)
+        few, few_last = ittt.causal_conv(X[:, :, at].contiguous(), w[at].contiguous(), b[at].contiguous(),
+                                         act="silu", state=s[:, :, at].contiguous(), lengths=n)
+        assert torch.equal(Y[:, :, at], few) and torch.equal(last[:, :, at], few_last)
+    ref, bound, last_ref = mx.causal_conv(host(X[:, :, :8]), host(w[:8]), host(b[:8]), "silu", host(s[:, :, :8]),
+                                          lengths, np.zeros((B, T, 8)))
+    within(Y[:, :, :8], ref, bound, dtype)
+    assert np.array_equal(host(last[:, :, :8]), last_ref)
+
+
 # ------------------------------------------------------------------- scan
 
 def scan_inputs(B, T, d, N, G, dtype, seed=0, softplus=True, lo=1e-3, hi=1e-1):
