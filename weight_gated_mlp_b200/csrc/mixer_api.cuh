@@ -439,7 +439,14 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   // B 1, d 512: 7.8 and 7.6 at T = 33.  B 32, d 1024, N 4: 57 and 97 at T = 256.)
   const double elements = double(p->B) * p->d * p->T * double((p->N + 3) / 4 * 4);
   const double serial_us = std::max(2.0 + 0.24 * p->T, 1.4e-6 * elements);
-  const double wave = c.passes == 2 ? 11.7 + 0.45 * p->N : 4.0 + 0.42 * p->N;
+  // Rows of channels that do not split into 16-byte pieces are staged element by element:
+  // 7 more a pass (B 9, T 3432, d 3033, N 4: 1526 in chunks, 28 a wave instead of 13.5;
+  // 739 token after token).
+  const int64_t V = p->dtype == ITTT_BF16 ? 8 : 4;
+  const bool pieces = (p->d / p->G) % V == 0 && stride_or(p->ldu, p->d) % V == 0 &&
+                      stride_or(p->ldt, p->d) % V == 0 && stride_or(p->ldz, p->d) % V == 0 &&
+                      stride_or(p->ldy, p->d) % V == 0;
+  const double wave = (c.passes == 2 ? 11.7 + 0.45 * p->N : 4.0 + 0.42 * p->N) + (pieces ? 0.0 : 7.0 * c.passes);
   const double chunk_us = std::max(c.passes == 2 ? 13.0 : 7.5,
                                    double(groups) * cdiv(p->T, kScanChunk) / workers * wave);
   c.short_call = p->T == 1 || serial_us < chunk_us;
