@@ -490,7 +490,7 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
     c.flags = take(size_t(1 + groups) * 4);
     c.carry = take(size_t(groups) * scan_ch(c.passes) * np * 4);
   } else {
-    c.carry = take(size_t(c.runs - 1) * p->B * p->d * p->N * 4);
+    c.carry = take(size_t(c.runs) * p->B * p->d * p->N * 4);
     c.step_sum = take(size_t(c.runs - 1) * p->B * p->d * 4);
   }
   c.total = off;

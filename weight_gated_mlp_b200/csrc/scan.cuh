@@ -305,8 +305,10 @@ struct ScanPlan {
   int runs;        // runs of run_tokens tokens (the last may be short)
   int run_tokens;  // a multiple of kScanChunk
   int chained;     // 1: a run starts from the state that the run before leaves in
-                   // `carry`; 0: run r from carry[r - 1] (filled by scan_join_kernel)
-  float* carry;    // chained: [B blocks][channels a block, NP]; else [runs - 1][B, d, N]
+                   // `carry`; 0: run r from carry[r] (filled by scan_join_kernel), run 0
+                   // too, since state_in may be the state_out that the last run's CTA,
+                   // which nothing orders behind run 0's, writes
+  float* carry;    // chained: [B blocks][channels a block, NP]; else [runs][B, d, N]
   float* step_sum; // state pass: [runs - 1][B, d], the runs' sums of s
   unsigned* flags; // chained: [0] the next task, [1 + B blocks] runs finished
 };
@@ -546,7 +548,8 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
     if (!first && t_begin >= len) {
       if constexpr (STATE_ONLY) {  // a run behind the end joins as nothing
         const long long at = ((long long)run * a.B + b) * a.d + c0;
-        for (int e = tid; e < nch * a.N; e += kScanThreads) pl.carry[at * a.N + e] = 0.f;
+        float* end = pl.carry + (at + (long long)a.B * a.d) * a.N;
+        for (int e = tid; e < nch * a.N; e += kScanThreads) end[e] = 0.f;
         if (tid < nch) pl.step_sum[at + tid] = 0.f;
       }
       continue;
@@ -591,9 +594,9 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
         A2 = a.A[(long long)(c0 + i) * a.N + n] * kLog2e;
         const long long at = ((long long)b * a.d + c0 + i) * a.N + n;
         if (!STATE_ONLY) {
-          if (first) h = a.state_in ? a.state_in[at] : 0.f;
-          else if (pl.chained) h = __ldcg(pl.carry + ((long long)gb * S::CH + i) * NP + n);
-          else h = pl.carry[(long long)(run - 1) * a.B * a.d * a.N + at];
+          if (pl.runs > 1 && !pl.chained) h = pl.carry[(long long)run * a.B * a.d * a.N + at];
+          else if (first) h = a.state_in ? a.state_in[at] : 0.f;
+          else h = __ldcg(pl.carry + ((long long)gb * S::CH + i) * NP + n);
         }
       }
       state[e] = h;
@@ -818,8 +821,8 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
     if (STATE_ONLY) {
       const long long at = ((long long)run * a.B + b) * a.d + c0;
       if (tid < nch) pl.step_sum[at + tid] = totals[tid];
-      for (int e = tid; e < nch * a.N; e += kScanThreads)
-        pl.carry[at * a.N + e] = state[(e / a.N) * NP + e % a.N];
+      float* end = pl.carry + (at + (long long)a.B * a.d) * a.N;  // carry[run + 1]
+      for (int e = tid; e < nch * a.N; e += kScanThreads) end[e] = state[(e / a.N) * NP + e % a.N];
       continue;
     }
     if (last) {
@@ -836,8 +839,9 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
   }
 }
 
-// Between the two passes: carry[run] becomes the state before run, from the runs'
-// own end states and sums of steps.
+// Between the two passes: carry[run + 1], which holds run's own end state, becomes the
+// state before run + 1, by the runs' sums of steps, and carry[0] the state before the
+// call.
 template <typename T_>
 __global__ void __launch_bounds__(256) scan_join_kernel(const ScanArgs<T_> a, const ScanPlan pl) {
   grid_dependency_wait();
@@ -846,10 +850,11 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanArgs<T_> a, co
   const long long bd = e / a.N;
   const float A2 = a.A[(bd % a.d) * a.N + e % a.N] * kLog2e;
   float h = a.state_in ? a.state_in[e] : 0.f;
+  pl.carry[e] = h;
   for (int r = 0; r < pl.runs - 1; ++r) {
-    const float end = pl.carry[r * total + e];
+    const float end = pl.carry[(r + 1) * total + e];
     h = fmaf(exp2_approx(pl.step_sum[(long long)r * a.B * a.d + bd] * A2), h, end);
-    pl.carry[r * total + e] = h;  // the state before run r + 1
+    pl.carry[(r + 1) * total + e] = h;
   }
 }
 
