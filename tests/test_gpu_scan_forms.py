@@ -87,6 +87,32 @@ def test_segments_of_independent_runs(dtype):
     within(s, h, hb, "f32")
 
 
+@pytest.mark.parametrize("start", ["zeros", "small"])
+@pytest.mark.parametrize("B,T,d,N,G,dtype,growth", [
+    (1, 28417, 250, 4, 1, "bf16", 19.0), (4, 4353, 48, 4, 2, "f32", 50.0), (1, 12289, 66, 4, 2, "bf16", 50.0)])
+def test_growth_past_the_range_over_a_run(B, T, d, N, G, dtype, growth, start):
+    """A > 0: every 256 tokens grow by at most e^growth, which fp32 holds, every run by
+    more than it holds.  Zeros first (a prompt padded in front), or a small state that
+    meets one such run and then ends."""
+    kind, runs, _ = form(B, T, d, N, G, dtype)
+    run = -(-(-(-T // 256)) // runs)                             # chunks of 256 tokens a run
+    assert kind == "runs" and growth < 88 < growth * run * 0.95
+    v = scan_inputs(B, T, d, N, G, dtype, seed=26, softplus=False)
+    v["delta"].fill_(0.0625)                                     # 16 in 256 tokens
+    v["A"] = torch.linspace(0.9, 1.0, d * N, device="cuda").reshape(d, N) * (growth / 16)
+    if start == "zeros":
+        v["U"][:, :T - 300] = 0
+        v["state"] = None
+        n = out = None
+    else:
+        v["U"].zero_()
+        v["state"] *= 1e-30
+        n = torch.full((B,), 256 * run + 3, dtype=torch.int32, device="cuda")
+        out = torch.zeros_like(v["U"])
+    Y, s = check_scan(v, dtype, lengths=n, out=out)
+    assert torch.isfinite(Y).all() and torch.isfinite(s).all()
+
+
 @pytest.mark.parametrize("B,T,d,N,G,dtype,want", [
     # the calls of test_gpu_mixer.py that are meant for a form
     (1, 3000, 16, 16, 1, "f32", "runs"), (2, 1500, 24, 8, 1, "bf16", "runs"), (1, 900, 40, 256, 1, "bf16", "runs"),

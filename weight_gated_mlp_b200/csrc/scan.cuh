@@ -853,7 +853,15 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const ScanArgs<T_> a, co
   pl.carry[e] = h;
   for (int r = 0; r < pl.runs - 1; ++r) {
     const float end = pl.carry[(r + 1) * total + e];
-    h = fmaf(exp2_approx(pl.step_sum[(long long)r * a.B * a.d + bd] * A2), h, end);
+    const float x = pl.step_sum[(long long)r * a.B * a.d + bd] * A2;
+    if (x > 126.f) {
+      // a run may grow by more than fp32 holds while what it multiplies is zero or small:
+      // three factors, none infinite (past 378 every h but 0 goes to infinity)
+      const float third = exp2_approx(fminf(x, 378.f) * (1.f / 3.f));
+      h = fmaf(third, third * (third * h), end);
+    } else {
+      h = fmaf(exp2_approx(x), h, end);
+    }
     pl.carry[(r + 1) * total + e] = h;
   }
 }
