@@ -4,17 +4,21 @@ marshalling module ``_marshal.so`` next to this file.
 ``python -m weight_gated_mlp_b200._build`` compiles ``csrc/api.cu`` (which
 includes every kernel header) with nvcc into a shared library exporting the
 C ABI of ``include/ittt.h``.  The CUDA runtime is linked statically.
-``csrc/marshal.cpp`` (g++, torch's headers) becomes the Python module through
-which the operators around the layer are called.
+``csrc/marshal.cpp`` (g++, torch's and Python's headers) becomes the Python module
+through which the operators around the layer are called; where these are
+missing, the library is built all the same and the module is left out.
 """
 
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -57,6 +61,36 @@ def marshal_command(out: str = MARSHAL) -> list:
             "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
 
 
+def marshal_lacks() -> Optional[str]:
+    """What the marshalling module needs and is not here; None: nothing."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if shutil.which("g++") is None:
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    return None
+
+
+def marshal_key() -> str:
+    """What the module is built against: Python's and torch's versions.  It stands in
+    a file beside the module, which is made again where they change."""
+    try:
+        torch_version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        from torch import __version__ as torch_version
+    return f"{sysconfig.get_config_var('SOABI')}, torch {torch_version}"
+
+
+def marshal_up_to_date() -> bool:
+    try:
+        with open(MARSHAL + ".key") as f:
+            built = f.read()
+    except OSError:
+        return False
+    return built == marshal_key() and newer(MARSHAL, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "ittt.h")])
+
+
 def newer(target: str, sources) -> bool:
     if not os.path.exists(target):
         return False
@@ -78,12 +112,18 @@ def run(cmd: list, target: str, what: str):
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if force or not newer(MARSHAL, [MARSHAL_SOURCE, os.path.join(ROOT, "include", "ittt.h")]):
-        run(marshal_command(MARSHAL + ".tmp"), MARSHAL, "g++")
     if force or not up_to_date():
         res = run(command(LIB + ".tmp", verbose_ptxas), LIB, "nvcc")
         if verbose_ptxas:
             sys.stderr.write(res.stderr)
+    lacks = marshal_lacks()
+    if lacks:
+        sys.stderr.write(f"{MARSHAL} not built, and with it linear, causal_conv and selective_scan in "
+                         f"Python: no {lacks}\n")
+    elif force or not marshal_up_to_date():
+        run(marshal_command(MARSHAL + ".tmp"), MARSHAL, "g++")
+        with open(MARSHAL + ".key", "w") as f:
+            f.write(marshal_key())
     return LIB
 
 
