@@ -425,10 +425,10 @@ ScanCut scan_cut(const ittt_scan_problem* p, int sms) {
   const long long workers = (long long)ctas * sms;
   // the wider channel blocks where they still fill the GPU (few, long sequences: as
   // independent runs), the narrow ones else; a state of more than one slab of B and C
-  // would be staged once a pass and gain nothing
+  // would be staged once a pass and gain nothing, and the kernel has no code for it
   const long long wide = p->B * p->G * cdiv(p->d / p->G, scan_ch(2));
   const bool few = wide * 4 < workers && cdiv(p->T, kScanChunk) * wide >= 4 * workers;
-  c.passes = p->dtype == ITTT_BF16 && p->N <= 16 && (wide >= workers || few) ? 2 : 1;
+  c.passes = p->dtype == ITTT_BF16 && p->N <= ScanShape<__nv_bfloat16, 2>::SLAB && (wide >= workers || few) ? 2 : 1;
   c.per_group = int(cdiv(p->d / p->G, scan_ch(c.passes)));
   c.blocks = c.per_group * p->G;
   const long long groups = p->B * c.blocks;

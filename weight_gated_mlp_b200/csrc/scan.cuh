@@ -291,7 +291,8 @@ constexpr int kScanThreads = 32 * kScanWarps;
 // Channels a CTA: a warp takes P pairs of channels one after the other.  Two halve
 // what staging B and C costs a channel (8 x 1024 x 5120 x 16: 436 us, 474 with one);
 // one makes twice as many tasks (1 x 8192 x 5120: 480 us, 543 with two, whose 320
-// channel blocks leave CTAs without work).
+// channel blocks leave CTAs without work).  Two are for a state of one slab of B and C,
+// which the second finds laid out.
 __host__ __device__ constexpr int scan_ch(int P) { return 2 * kScanWarps * P; }
 constexpr int kScanK = 8;                // tokens a span, one span a lane
 constexpr int kScanChunk = 32 * kScanK;  // tokens a chunk
@@ -608,7 +609,6 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
       skips[tid] = (a.D && tid < nch) ? a.D[c0 + tid] : 0.f;
       totals[tid] = 0.f;
     }
-    const bool one_slab = NP <= S::SLAB;
 
     for (int t0 = t_begin; t0 < t_end; t0 += kScanChunk) {
       const int tokens = min(kScanChunk, t_end - t0);
@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
         const bool last_pass = pass == P - 1;
 #pragma unroll 1
         for (int n0 = 0; n0 < NP; n0 += S::SLAB) {
-          const bool fresh = pass == 0 || !one_slab;  // else B and C are laid out already
+          const bool fresh = pass == 0;  // else B and C, one slab, are laid out already
           if (fresh) {
             copy_wait<0>();
             __syncthreads();  // the copies are in; the tiles' readers of the step before are done
@@ -687,9 +687,7 @@ __global__ void __launch_bounds__(kScanThreads, ScanShape<T_, P>::CTAS)
           // what comes next arrives during the recurrences
           if (n0 + S::SLAB < NP) {
             fetch_bc(t0, n0 + S::SLAB);
-          } else if (!last_pass) {
-            if (!one_slab) fetch_bc(t0, 0);
-          } else if (t0 + kScanChunk < t_end) {
+          } else if (last_pass && t0 + kScanChunk < t_end) {
             fetch_inputs(t0 + kScanChunk);
             fetch_bc(t0 + kScanChunk, 0);
           }
