@@ -81,6 +81,8 @@ ittt_status launch_clusters(void (*kern)(KArgs...), unsigned grid, unsigned clus
   return launch_status();
 }
 
+constexpr int kSmemMost = 232448;  // the most dynamic shared memory of a CTA
+
 // Dynamic shared memory above the default, granted once per kernel and device.
 template <typename Kern>
 bool grant_smem(Kern kern, int smem, std::atomic<bool>* done) {
@@ -137,34 +139,77 @@ ittt_status linear_f32(const LinearArgs<float>& a, cudaStream_t st) {
   return linear_f32_sized<ACT, false>(a, sms, st);
 }
 
-// Dynamic shared memory that spreads `ctas` CTAs evenly: as much as lets no SM hold more
-// of them than the fullest one has to.  Clusters are otherwise packed onto fewer SMs
-// (777 x 5120 x 192, 208 CTAs: 8.6 us, 10.1 without).
-int spread_smem(long long ctas, int sms, int need) {
-  const long long per_sm = std::max(1ll, cdiv(ctas, sms));
-  const long long share = 233472 / per_sm - 1024;  // an SM's shared memory; 1 KB a CTA is reserved
-  return int(std::max<long long>(need, std::min<long long>(share, 232448) / 1024 * 1024));
+// Never launched: place_kernel stands in for linear_split_kernel in questions about how
+// many clusters fit, which for a kernel with tensor memory are answered as if an SM
+// held one CTA of it.
+__global__ void __launch_bounds__(192) place_kernel() {}
+
+// Dynamic shared memory at which an SM holds `per_sm` CTAs and no more (1 KB of an SM's 228
+// is reserved for each).
+int smem_for(int per_sm) { return std::min(kSmemMost, (233472 / per_sm - 1024) / 1024 * 1024); }
+
+// Clusters of `cluster` CTAs that the current device holds at once with per_sm CTAs an SM
+// (0: it does not say).  Fewer than the SMs divided, since no cluster leaves its part of the
+// GPU: of 8, 15 at one CTA an SM, 33 at two and 48 at three, where 148 SMs would give 18,
+// 37 and 55.
+int cluster_places(int per_sm, int cluster) {
+  static std::atomic<bool> granted[kMaxDevices] = {};
+  static std::atomic<int> known[kMaxDevices][4][9] = {};
+  if (!grant_smem(place_kernel, kSmemMost, granted)) return 0;
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::atomic<int>& places = known[dev][per_sm][cluster];
+  if ((n = places.load(std::memory_order_relaxed)) > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(unsigned(cluster) * 1024, 1, 1);
+  cfg.blockDim = dim3(192, 1, 1);
+  cfg.dynamicSmemBytes = smem_for(per_sm);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, place_kernel, &cfg) != cudaSuccess || n <= 0) return 0;
+  places.store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // One 128 x MT tile per CTA, K split over clusters.  The split is the widest of
-// 1, 2, 4, 8 CTAs that leaves every CTA of the launch resident and at least four
-// k-blocks to each.
+// 1, 2, 4, 8 CTAs whose clusters the GPU holds all at once and that leaves at least four
+// k-blocks to each CTA.  A call asks for the shared memory that lets no SM hold more CTAs
+// than that takes: clusters are otherwise packed onto fewer SMs (777 x 5120 x 192, 208
+// CTAs: 12.8 us, 13.7 without).  Counted by SMs alone, clusters that found no place ran
+// behind the others (1 x 9728 x 2304, 18 clusters of 8: 20.3 us, 11.9 in two CTAs an SM; 1
+// x 4096 x 6400, 50 of 8: 15.7 us, 12.3 in clusters of 4).
 template <int MT, int ACT>
 ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream_t st) {
   using S = SplitShape<MT>;
   static std::atomic<bool> granted[kMaxDevices] = {};
   auto kern = linear_split_kernel<MT, ACT>;
-  if (!grant_smem(kern, 232448, granted)) return ITTT_ERR_CUDA;
+  if (!grant_smem(kern, kSmemMost, granted)) return ITTT_ERR_CUDA;
   const int num_kb = int(cdiv(a.K, 64));
   const long long m_tiles = cdiv(a.M, MT), tiles = m_tiles * cdiv(a.N, 128);
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= (long long)S::CTAS * sms && num_kb >= 4 * splits * 2) splits *= 2;
+  int splits = 1, per_sm = 1;
+  while (splits < 8 && num_kb >= 4 * splits * 2) {
+    const int places = cluster_places(S::CTAS, splits * 2);
+    if (places <= 0) return ITTT_ERR_CUDA;
+    if (tiles > places) break;
+    splits *= 2;
+  }
+  while (per_sm < S::CTAS) {
+    const int places = splits == 1 ? per_sm * sms : cluster_places(per_sm, splits);
+    if (places <= 0) return ITTT_ERR_CUDA;
+    if (tiles <= places) break;
+    ++per_sm;
+  }
   if (tiles * splits >= (1ll << 31)) return ITTT_ERR_UNSUPPORTED;
   CUtensorMap w, x;
   if (!make_map(&w, a.W, a.K, a.N, a.K, 64, 128) || !make_map(&x, a.X, a.K, a.M, a.ldx, 64, MT))
     return ITTT_ERR_CUDA;
   return launch_clusters(kern, unsigned(tiles * splits), unsigned(splits), 192,
-                         spread_smem(tiles * splits, sms, S::SMEM), st, w, x, a,
+                         std::max(S::SMEM, smem_for(per_sm)), st, w, x, a,
                          int(m_tiles), num_kb, g_wait_ns.load());
 }
 
