@@ -180,9 +180,12 @@ int cluster_places(int per_sm, int cluster) {
 // 1, 2, 4, 8 CTAs whose clusters the GPU holds all at once and that leaves at least four
 // k-blocks to each CTA.  A call asks for the shared memory that lets no SM hold more CTAs
 // than that takes: clusters are otherwise packed onto fewer SMs (777 x 5120 x 192, 208
-// CTAs: 12.8 us, 13.7 without).  Counted by SMs alone, clusters that found no place ran
-// behind the others (1 x 9728 x 2304, 18 clusters of 8: 20.3 us, 11.9 in two CTAs an SM; 1
-// x 4096 x 6400, 50 of 8: 15.7 us, 12.3 in clusters of 4).
+// CTAs: 12.8 us, 13.7 without).  Two CTAs always find room, so that the next launch's, or
+// another stream's, can start beside a CTA that has its SM to itself (128 x 4096 x 1024, 64
+// CTAs: 10.2 us in a chain of calls, 10.5 where the memory let an SM hold one).  Counted by
+// SMs alone, clusters that found no place ran behind the others (1 x 9728 x 2304, 18
+// clusters of 8: 20.3 us, 12.2 in two CTAs an SM; 1 x 4096 x 6400, 50 of 8: 15.7 us, 12.3 in
+// clusters of 4).
 template <int MT, int ACT>
 ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream_t st) {
   using S = SplitShape<MT>;
@@ -191,7 +194,7 @@ ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream
   if (!grant_smem(kern, kSmemMost, granted)) return ITTT_ERR_CUDA;
   const int num_kb = int(cdiv(a.K, 64));
   const long long m_tiles = cdiv(a.M, MT), tiles = m_tiles * cdiv(a.N, 128);
-  int splits = 1, per_sm = 1;
+  int splits = 1, per_sm = 2;
   while (splits < 8 && num_kb >= 4 * splits * 2) {
     const int places = cluster_places(S::CTAS, splits * 2);
     if (places <= 0) return ITTT_ERR_CUDA;
