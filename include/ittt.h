@@ -403,7 +403,8 @@ ittt_status ittt_lm_target_noalloc(const ittt_problem* p, const void* X0, const 
  * and into decoding.  Inference only, as everything here.  The conventions
  * above hold, with these differences: matrices whose rows are tokens may be
  * column slices of wider ones (a row stride in elements; 0 = dense rows), and
- * optional tensors are passed as NULL. */
+ * optional tensors are passed as NULL.  Rows (M, B T) and widths (N, K, d, G N, the
+ * row strides) are below 2^31 - 1024; sizes past a limit give ITTT_ERR_UNSUPPORTED. */
 
 typedef enum {
   ITTT_ACT_NONE = 0,
@@ -457,7 +458,8 @@ typedef struct {
  * NULL: sequence b has lengths[b] tokens in this call (clamped to 0..T); the
  * rows behind them are not read, and their rows of Y are left as they were.
  * Y must not overlap another tensor, state_out none but state_in.  One rounding, on
- * the store. */
+ * the store.  B <= 65535, T <= 2^30 (with more than 8 taps 2^20 - 32), and
+ * B ceil(T / 8) d < 2^32 - 128. */
 ittt_status ittt_causal_conv(const ittt_conv_problem* p, const void* X, const void* conv_kernel,
                              const void* bias, const void* state_in, const int32_t* lengths,
                              void* Y, void* state_out, void* stream);
@@ -494,7 +496,7 @@ ittt_status ittt_selective_scan_workspace_size(const ittt_scan_problem* p, size_
  * float32 (NULL: not wanted) h after each sequence's last one, and may be
  * state_in itself.  lengths as for ittt_causal_conv (a sequence of length 0
  * passes its state through).  Y must not overlap another tensor, state_out none but
- * state_in.  Everything is
+ * state_in.  B and T <= 2^30, B d < 2^31.  Everything is
  * computed and held in fp32; Y is rounded once.  Made for decay, s A <= 0: where
  * s A > 0, the growth over any 256 tokens has to stay within fp32's range, and
  * what leaves that range comes out inf or NaN. */

@@ -1,6 +1,5 @@
-// Kernels of the operators around the layer: the product with bias, activation
-// and residual, the short causal convolution and the selective state space
-// scan.
+// What the kernels of the operators around the layer share (conversions, activations,
+// paired arithmetic), and the short causal convolution.
 #pragma once
 
 #include <type_traits>
@@ -131,7 +130,7 @@ __device__ __forceinline__ int sequence_length(const int32_t* lengths, int b, in
 }
 
 // Bound by reading X and writing Y once, with the activation's two special-function
-// results a value close behind: 8192 x 5120 in bf16 with four taps and silu 35.2 us, 4.8
+// results a value close behind: 8192 x 5120 in bf16 with four taps and silu 35.3 us, 4.75
 // TB/s (torch's copy of the same bytes 27.2 us; 37.3 us with one channel an instruction
 // and eight steps a thread).  A thread owns V neighbouring channels (16 bytes; 1
 // where widths or alignment do not allow that) over `steps` times four tokens.  It

@@ -1,5 +1,6 @@
-// C ABI of the operators around the layer (validation and dispatch of the
-// kernels of mixer.cuh).  Included at the end of api.cu, whose helpers it uses.
+// C ABI of the operators around the layer: validation, and dispatch of the kernels of
+// tc_linear.cuh, linear_f32.cuh, mixer.cuh and scan.cuh.  Included at the end of api.cu,
+// whose helpers it uses.
 #pragma once
 
 namespace {
@@ -262,9 +263,10 @@ ittt_status linear_pairs(const LinearArgs<__nv_bfloat16>& a, int pairs, cudaStre
 
 // Up to 128 rows: one narrow tile of all rows per 128 outputs, so that W is read
 // once.  More: split tiles of 128 x 128 while K can still be split over two CTAs (the
-// pairs' 256 x 256 tiles leave most SMs empty there: 512 x 9728 x 2560 takes 48 us
-// split and 61 in pairs), of 128 x 64 where even eight-fold splits of those leave SMs
-// empty; from there on pairs (1024 x 9728 x 2560: 61 us, 80 us in unsplit tiles).
+// pairs' 256 x 256 tiles leave most SMs empty there: 512 x 9728 x 2560 takes 40 us
+// split and 50 in pairs, but 69 and 56 with a residual, which the split's join loads a
+// row at a time), of 128 x 64 where even eight-fold splits of those leave SMs empty;
+// from there on pairs (1024 x 9728 x 2560: 52 us, 80 us in unsplit tiles).
 template <int ACT>
 ittt_status linear_bf16(const LinearArgs<__nv_bfloat16>& a, cudaStream_t st) {
   const int sms = num_sms();

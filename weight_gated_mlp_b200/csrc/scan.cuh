@@ -3,10 +3,12 @@
 //   y_t[c]    = sum_n h_t[c, n] C_t[n] + D[c] u_t[c],  Y = y silu(z).
 //
 // One exponential per state element and token is the largest cost (the unit that
-// computes it takes 16 a clock and SM), so no kernel computes one twice.
+// computes it takes 16 a clock and SM), so no pass over the tokens computes one twice.  A
+// call that is cut into independent runs makes two passes over all runs but the last,
+// and a join costs one exponential more for 8 tokens.
 //
 //   scan_token_kernel   single tokens: lanes over the state, sequence after sequence.
-//       Bound by the state's bytes (64 sequences of 5120 x 16: 12.9 us, 6.9 us at HBM's
+//       Bound by the state's bytes (64 sequences of 5120 x 16: 13.7 us, 6.9 us at HBM's
 //       copy rate).
 //   scan_serial_kernel  short calls: lanes over the state, four or eight elements a
 //       lane, four tokens at a time.  Bound by the latency of one token after the other

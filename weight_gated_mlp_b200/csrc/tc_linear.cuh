@@ -13,13 +13,13 @@
 //       rank order (the same bits every time, no workspace, one launch).  For few
 //       rows it is bound by reading W once from HBM, and by what a launch costs before
 //       its first bytes arrive and after its last: 1 x 9728 x 2560 with bias and residual
-//       11.8 us (4.2 TB/s; 7.6 us at HBM's copy rate), 64 x 2560 x 10240 14.4 us (8.3).
+//       12.3 us (4.0 TB/s; 7.6 us at HBM's copy rate), 64 x 2560 x 10240 15.5 us (8.3).
 //   linear_pair_kernel   persistent CTA pairs (two SMs, one 256-lane tile, 256
 //       columns, two TMEM slots so that a tile's epilogue overlaps the next tile's main
-//       loop).  For many rows: bound by the tensor cores.  8192 x 9728 x 2560: 334 us in
-//       a loop of calls, 1.22 PFLOP/s (cuBLAS's bare product 267 us); under the power
-//       cap, where the measured peak is 1.40 PFLOP/s, that is 0.87 of it.  Its last wave
-//       is part full (320 tiles on 74 pairs).
+//       loop).  For many rows: bound by the tensor cores.  8192 x 9728 x 2560 with
+//       residual: 349 us in a loop of calls, 1.17 PFLOP/s (cuBLAS's bare product 267 us);
+//       under the power cap, where the measured peak is 1.40 PFLOP/s, that is 0.83 of it.
+//       Its last wave is part full (320 tiles on 74 pairs).
 #pragma once
 
 #include "common.cuh"
