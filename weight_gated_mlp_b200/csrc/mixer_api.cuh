@@ -150,15 +150,15 @@ __global__ void __launch_bounds__(192) place_kernel() {}
 int smem_for(int per_sm) { return std::min(kSmemMost, (233472 / per_sm - 1024) / 1024 * 1024); }
 
 // Clusters of `cluster` CTAs that the current device holds at once with per_sm CTAs an SM
-// (0: it does not say).  Fewer than the SMs divided, since no cluster leaves its part of the
+// (-1: it does not say).  Fewer than the SMs divided, since no cluster leaves its part of the
 // GPU: of 8, 15 at one CTA an SM, 33 at two and 48 at three, where 148 SMs would give 18,
 // 37 and 55.
 int cluster_places(int per_sm, int cluster) {
   static std::atomic<bool> granted[kMaxDevices] = {};
   static std::atomic<int> known[kMaxDevices][4][9] = {};
-  if (!grant_smem(place_kernel, kSmemMost, granted)) return 0;
+  if (!grant_smem(place_kernel, kSmemMost, granted)) return -1;
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
   std::atomic<int>& places = known[dev][per_sm][cluster];
   if ((n = places.load(std::memory_order_relaxed)) > 0) return n;
   cudaLaunchConfig_t cfg = {};
@@ -172,7 +172,7 @@ int cluster_places(int per_sm, int cluster) {
   cfg.dynamicSmemBytes = smem_for(per_sm);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, place_kernel, &cfg) != cudaSuccess || n <= 0) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, place_kernel, &cfg) != cudaSuccess) return -1;
   places.store(n, std::memory_order_relaxed);
   return n;
 }
@@ -198,13 +198,13 @@ ittt_status linear_split(const LinearArgs<__nv_bfloat16>& a, int sms, cudaStream
   int splits = 1, per_sm = 2;
   while (splits < 8 && num_kb >= 4 * splits * 2) {
     const int places = cluster_places(S::CTAS, splits * 2);
-    if (places <= 0) return ITTT_ERR_CUDA;
+    if (places < 0) return ITTT_ERR_CUDA;
     if (tiles > places) break;
     splits *= 2;
   }
   while (per_sm < S::CTAS) {
     const int places = splits == 1 ? per_sm * sms : cluster_places(per_sm, splits);
-    if (places <= 0) return ITTT_ERR_CUDA;
+    if (places < 0) return ITTT_ERR_CUDA;
     if (tiles <= places) break;
     ++per_sm;
   }
